@@ -519,6 +519,236 @@ dsa_status dsa_decode_noalloc(const void *q_idx, const float *q_scale, const voi
                               uint32_t *status_out, void *stream);
 
 /*
+ * Speculative decoding over the paged caches.  None of the pages describes
+ * it; it is the usual companion of the paged decode above: a cheap drafter
+ * proposes a tree of tokens for every sequence, the model scores the whole
+ * tree in one pass, and the longest path that the target's probabilities
+ * accept is kept.  One step of B sequences, all on the device:
+ *   1. dsa_blocks_extend reserves cache slots for the drafts: pages from the
+ *      free list into the block tables, and each token's sequence, position
+ *      and slot (seq_ids and positions as dsa_cache_append takes them);
+ *   2. dsa_rope rotates the new queries and keys to their positions (a tree
+ *      token's position for the rotation is the prefix plus its depth);
+ *   3. dsa_cache_append writes the new rows into the caches;
+ *   4. dsa_tree_attn attends every drafted token over the cached prefix, its
+ *      ancestors in the tree and itself;
+ *   5. dsa_verify_tree walks the tree and samples the next token;
+ *   6. dsa_cache_compact moves the accepted path's cache rows together;
+ *   7. dsa_blocks_trim gives the other pages back.
+ * The drafted tokens of all sequences are packed: token_start int32 [B + 1],
+ * ascending from 0, and sequence b's tokens are token_start[b] ..
+ * token_start[b + 1] - 1.  `parents` int32, one per token: the parent's index
+ * within its sequence (smaller than the token's own), -1 for a token that
+ * follows the cached prefix, below -1 for a padding row.  Trees have at most
+ * DSA_MAX_TREE tokens.  `context_lens` counts the drafts in: token i of
+ * sequence b sits in the cache at position context_lens[b] - n_b + i, n_b
+ * being its number of tokens.
+ */
+#define DSA_MAX_TREE 128
+
+/*
+ * dsa_blocks_extend -- block tables and slot maps from request lengths.  The
+ * pool, all device memory, updated in place:
+ *   block_table  int32 [B, max_pages_per_seq]; context_lens int32 [B] (tokens
+ *   cached); pages_held int32 [B] (pages in the table); free_pages int32
+ *   [free_capacity], a stack of free page ids, its top at free_count - 1;
+ *   free_count int32 [1].
+ * Sequence b grows by new_lens[b] >= 0 tokens.  With ps = page_size it needs
+ *   need_b = max(0, ceil((context_lens[b] + new_lens[b]) / ps) - pages_held[b])
+ * pages (0 when new_lens[b] is 0), taken from the top of the stack in the
+ * order of the sequences and of their pages.  Then context_lens, pages_held and
+ * free_count hold the new values, and (outputs)
+ *   token_start int32 [B + 1]: first packed token of each sequence;
+ *   seq_ids, positions int32 [max_tokens], slots int64 [max_tokens] (nullable):
+ *   each new token's sequence, position in it and cache row (page * ps +
+ *   position % ps); -1 behind the last token.
+ * Refused, with context_lens and the rest left as they were and no tokens:
+ * a sequence whose numbers are negative or inconsistent (pages_held * ps <
+ * context_lens) or which would outgrow its table (DSA_ERR_INVALID_ARG in
+ * *status), one that the pages left by the sequences before it do not serve,
+ * and one that would pass max_tokens (DSA_ERR_WORKSPACE; later sequences that
+ * need pages, or have tokens, are then refused too).  A page id outside
+ * [0, num_pages) is reported as DSA_ERR_INVALID_ARG and stands as slot -1.
+ * status: device uint32_t the caller zeroes beforehand, nullable; the first
+ * error stays.  Pointers 16-byte aligned (free_count and status 4-byte).
+ * Requires num_pages * page_size < 2^31.  B == 0 is a no-op.
+ */
+dsa_status dsa_blocks_extend(const int32_t *new_lens, int32_t *context_lens, int32_t *pages_held,
+                             int32_t *block_table, const int32_t *free_pages, int64_t free_capacity,
+                             int32_t *free_count, int B, int max_pages_per_seq, int64_t num_pages, int page_size,
+                             int64_t max_tokens, int32_t *token_start, int32_t *seq_ids, int32_t *positions,
+                             int64_t *slots, uint32_t *status, void *stream);
+
+/*
+ * dsa_blocks_trim -- cuts every sequence back to keep_lens[b] tokens (the
+ * accepted ones, or 0 for a request that is done; 0 <= keep_lens[b] <=
+ * context_lens[b]).  context_lens becomes keep_lens; the pages behind
+ * ceil(keep_lens / page_size) go back on the free stack, their table entries
+ * become -1, and pages_held and free_count follow.  They are pushed in
+ * reverse, so that trimming to the old lengths undoes a dsa_blocks_extend
+ * exactly.  A sequence with a length out of range, or pages_held outside
+ * [0, max_pages_per_seq], is left alone (DSA_ERR_INVALID_ARG in *status); so
+ * are sequences whose pages would pass free_capacity, and the ones behind
+ * them that free pages (DSA_ERR_WORKSPACE).  A table entry outside
+ * [0, num_pages) is pushed as -1 and reported.  Pool, status and alignment as
+ * in dsa_blocks_extend.  B == 0 is a no-op.
+ */
+dsa_status dsa_blocks_trim(const int32_t *keep_lens, int32_t *context_lens, int32_t *pages_held,
+                           int32_t *block_table, int32_t *free_pages, int64_t free_capacity, int32_t *free_count,
+                           int B, int max_pages_per_seq, int64_t num_pages, int page_size, uint32_t *status,
+                           void *stream);
+
+/*
+ * dsa_rope_freqs -- frequency table of rotary positions (HOST memory, no GPU
+ * work): turns_out[i], i < rot_dim / 2, is the rotation per position of pair
+ * i in units of 2^-64 turns,
+ *   round(2^64 * f_i / (2 pi)),  f_i = base^(-2 i / rot_dim)   (DSA_ROPE_NONE)
+ *   f_i / factor                                               (DSA_ROPE_LINEAR)
+ *   f_i (1 - r_i) + f_i / factor * r_i                         (DSA_ROPE_YARN)
+ * with r_i = clamp((i - low) / max(high - low, 0.001), 0, 1), low =
+ * max(floor(t(beta_fast)), 0), high = min(ceil(t(beta_slow)), rot_dim - 1) and
+ * t(b) = rot_dim ln(original_context / (2 pi b)) / (2 ln base): pairs that
+ * turn more than beta_fast times within the original context keep their
+ * frequency, those under beta_slow turns are interpolated.  Whole turns drop
+ * out of the product position * turns, so angles keep their precision at any
+ * position.  Requires rot_dim even, 2 .. 256, base > 1, factor >= 1 (scaled
+ * forms), original_context >= 1, beta_fast > beta_slow > 0 (YaRN).
+ */
+typedef enum dsa_rope_scaling { DSA_ROPE_NONE = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_YARN = 2 } dsa_rope_scaling;
+dsa_status dsa_rope_freqs(int rot_dim, double base, dsa_rope_scaling scaling, double factor,
+                          int64_t original_context, double beta_fast, double beta_slow, uint64_t *turns_out);
+
+/*
+ * dsa_rope -- rotary positions of queries and keys in one launch.  q is
+ * [rows, H_q, d] and k [rows, H_k, d] (k NULL with H_k 0: queries only), bf16
+ * (DSA_BF16) or fp32 (DSA_F32), heads dense, rows q_stride / k_stride elements
+ * apart (so that both may lie in one projection's output).  In every head the
+ * elements rot_begin .. rot_begin + rot_dim - 1 are rotated, pair by pair:
+ *   (a, c) -> attn_factor (a cos - c sin, c cos + a sin),
+ *   angle = 2 pi positions[row] turns[i] / 2^64,
+ * pair i being elements (2i, 2i + 1) of that part (interleaved != 0) or
+ * (i, i + rot_dim / 2) (interleaved == 0); the other elements are copied.
+ * `turns` is a HOST table of rot_dim / 2 entries (dsa_rope_freqs), read before
+ * the call returns.  inverse != 0 rotates by minus the angle: with the same
+ * attn_factor it is the gradient of the forward call (the transpose).
+ * positions int32 [rows], any value.  Outputs have their own row strides;
+ * q_out == q (k_out == k) with equal strides rotates in place, any other
+ * overlap is undefined.  Angles are good to 2^-27 turns, sine and cosine
+ * fp32, products fp32, one rounding to the output type.
+ * Requires d a multiple of 8 up to 1024, rot_begin a multiple of 8, rot_dim a
+ * multiple of 16 up to 256, rot_begin + rot_dim <= d (else
+ * DSA_ERR_UNSUPPORTED); strides multiples of 8 and at least H * d; 16-byte
+ * aligned pointers (positions 4-byte).  rows == 0 is a no-op.
+ */
+dsa_status dsa_rope(const void *q, int64_t q_stride, int H_q, const void *k, int64_t k_stride, int H_k,
+                    const int32_t *positions, int64_t rows, int d, int rot_begin, int rot_dim, int interleaved,
+                    const uint64_t *turns, float attn_factor, int inverse, void *q_out, int64_t q_out_stride,
+                    void *k_out, int64_t k_out_stride, dsa_dtype dtype, void *stream);
+
+/*
+ * dsa_tree_attn -- softmax attention of the drafted tokens over the paged K/V
+ * caches (the whole cached prefix, not a selection: what DSA computes where
+ * the context is not longer than k, and what a dense drafter or a dense layer
+ * needs).  Query t = token i of sequence b attends positions s <
+ * context_lens[b] - n_b, and the cache rows of its ancestors and itself:
+ *   out[t, h] = sum_s softmax_s(sm_scale q[t, h] . K[s, h / (H_q / H_kv)]) V[s, ...]
+ *   q [N, H_q, d] bf16 packed by token_start; token_start [B + 1], parents [N],
+ *   context_lens [B], block_table [B, max_pages_per_seq] int32 as above;
+ *   k_cache, v_cache: bf16 [num_pages, page_size, H_kv, d] (scales NULL), or
+ *   E4M3 codes (uint8, the same shape) with k_cache_scale, v_cache_scale f32
+ *   [num_pages, page_size, H_kv] both given (H_kv == 1: dsa_cache_append's and
+ *   dsa_cache_append_kv8's layouts).
+ * Outputs: out bf16 [N, H_q, d]; lse_out f32 [N, H_q] (nullable), the natural
+ * log-sum-exp of the scaled logits.  A padding row (and a row under one) gives
+ * zeros and -inf.  Rows of tokens outside every sequence, and of sequences
+ * that are reported, are left as they were.
+ * max_tree (<= DSA_MAX_TREE) and max_context bound every n_b and every
+ * context_lens[b].  Through dsa_stream_status: DSA_ERR_INVALID_ARG for a
+ * sequence with token_start out of order or past N, more than max_tree tokens,
+ * or a context outside [n_b, min(max_context, max_pages_per_seq * page_size)]
+ * (skipped; nothing is checked where n_b is 0), for a parent not below its
+ * child (the row counts as padding), and for a page id out of range (its
+ * positions count as rows of zeros).  Cache rows at and behind
+ * context_lens[b] have no effect, whatever they hold; K and V of the
+ * positions before it must be finite.
+ * FP8 caches: K's scale is applied to the fp32 logits and V's to the fp32
+ * weights, so that the codes enter the products exactly; weights are rounded
+ * to bf16 once, as with bf16 caches.
+ * Supported: d 64 or 128, page_size a multiple of 16, H_q a multiple of H_kv,
+ * B <= 65536, num_pages * page_size < 2^31 (else DSA_ERR_UNSUPPORTED);
+ * sm_scale finite and > 0.  N == 0 is a no-op.  workspace: at least
+ * dsa_tree_attn_workspace_size(...) bytes, 256-byte aligned; calls that may
+ * overlap need one each.
+ */
+size_t dsa_tree_attn_workspace_size(int B, int64_t N, int H_q, int H_kv, int d);
+dsa_status dsa_tree_attn(const void *q, const void *k_cache, const float *k_cache_scale, const void *v_cache,
+                         const float *v_cache_scale, const int32_t *block_table, const int32_t *context_lens,
+                         const int32_t *token_start, const int32_t *parents, int64_t num_pages,
+                         int max_pages_per_seq, int page_size, int B, int64_t N, int max_tree, int64_t max_context,
+                         int H_q, int H_kv, int d, float sm_scale, void *out, float *lse_out, void *workspace,
+                         size_t ws_bytes, void *stream);
+
+/*
+ * dsa_verify_tree -- verification of drafted tokens against the target's
+ * probabilities, from given random numbers.  Node i of sequence b is packed
+ * row token_start[b] + i; node 0 is the last confirmed token, always kept.
+ *   target_probs f32 [N, V]: row t is the target's distribution of the token
+ *   that follows node t; draft_probs f32 [N, V]: row t is the distribution
+ *   that the children of node t were drawn from, independently of each other
+ *   (NULL: they were chosen without chance, a point mass on each);
+ *   tokens, parents int32 [N]; u_accept f32 [N], u_sample f32 [B] in [0, 1).
+ * From the current node u (first node 0), with R = P_u (its target row) and
+ * Z = 1, the children c of u are tried in order of their index:
+ *   accept c if u_accept[c] * Q(x_c) * Z < R(x_c): c becomes the current node;
+ *   else R <- max(R / Z - Q, 0) and Z <- sum R (both unchanged if that sum is
+ *   not above 0), Q being draft row u or the point mass on x_c.
+ * When no child is left the next token is drawn from R: the smallest v with
+ * sum_{v' <= v} R(v') > u_sample[b] * sum R.  The emitted tokens then follow
+ * the target's distribution exactly.
+ * Sums and comparisons are in 64 bits, in a fixed order: a call repeats bit
+ * for bit.  Outputs: path_out int32 [B, max_path]: the kept nodes, node 0
+ * first, then -1 (at most max_path nodes: the walk ends there);
+ * accept_len int32 [B]: how many; next_token int32 [B].  A sequence without
+ * tokens gets accept_len 0 and next_token -1; so does one that is reported as
+ * DSA_ERR_INVALID_ARG in *status (token_start out of order or past N, more
+ * than DSA_MAX_TREE tokens).  A child with a token outside [0, V) is rejected
+ * without a change of R and reported.  If R has no positive finite sum,
+ * next_token is -1, reported too.
+ * status: device uint32_t the caller zeroes beforehand, nullable.  Pointers
+ * 16-byte aligned (status 4-byte).  Requires 1 <= V < 2^31, max_path >= 1.  B == 0
+ * is a no-op; N == 0 needs no rows.
+ */
+dsa_status dsa_verify_tree(const float *target_probs, const float *draft_probs, const int32_t *tokens,
+                           const int32_t *parents, const int32_t *token_start, const float *u_accept,
+                           const float *u_sample, int B, int64_t N, int64_t V, int max_path, int32_t *path_out,
+                           int32_t *accept_len, int32_t *next_token, uint32_t *status, void *stream);
+
+/*
+ * dsa_cache_compact -- moves the cache rows of the accepted paths together:
+ * with first_b = context_lens[b] - n_b, the rows at position first_b +
+ * path[b, i] become the rows at first_b + i, for i < accept_len[b] (path int32
+ * [B, max_path] ascending, as dsa_verify_tree writes it), in every cache given:
+ *   kidx_cache uint8 [num_pages, page_size, d_I] with kscale_cache f32
+ *   [num_pages, page_size] (both NULL: none); k_cache, v_cache bf16
+ *   [num_pages, page_size, d], or uint8 with k_cache_scale, v_cache_scale f32.
+ * keep_lens_out int32 [B] (nullable): first_b + accept_len[b], the length to
+ * trim to.  context_lens and the block tables are not changed.  A sequence
+ * whose token_start, context, accept_len or path is out of range or not
+ * ascending is left alone, its keep_lens_out being context_lens[b], and
+ * DSA_ERR_INVALID_ARG is written to *status (as in dsa_cache_append); so is
+ * one with a page id outside [0, num_pages) among the rows to move.
+ * Supported: d_I a multiple of 8, d a multiple of 8 (kv8) or 4; caches 8-byte
+ * aligned; at most DSA_MAX_TREE tokens a sequence.
+ * B == 0 is a no-op.
+ */
+dsa_status dsa_cache_compact(const int32_t *block_table, const int32_t *context_lens, const int32_t *token_start,
+                             const int32_t *path, const int32_t *accept_len, int B, int64_t N, int max_path,
+                             int max_pages_per_seq, int64_t num_pages, int page_size, int d_I, int d,
+                             void *kidx_cache, float *kscale_cache, void *k_cache, float *k_cache_scale,
+                             void *v_cache, float *v_cache_scale, int32_t *keep_lens_out, uint32_t *status,
+                             void *stream);
+
+/*
  * Stage timing -- a tracing aid with no counterpart on the pages.  While
  * enabled (process-wide), dsa_prefill and dsa_prefill_host record a pair of
  * CUDA events on their stream around each stage's launches; the events are

@@ -193,4 +193,35 @@ cudaError_t launch_merge_partials(const uint16_t *part_out, int64_t out_stride, 
                                   int64_t lse_stride, int G, int B, int H, int d, uint16_t *out, float *lse,
                                   cudaStream_t st);
 
+// ---- speculative decoding (rope.cu, blocks.cu, tree_attn.cu, verify.cu) ----
+cudaError_t launch_rope(const void *q, int64_t q_stride, int H_q, const void *k, int64_t k_stride, int H_k,
+                        const int32_t *positions, int64_t rows, int d, int rot_begin, int rot_dim, bool interleaved,
+                        const uint64_t *turns, float factor, bool inverse, void *q_out, int64_t q_out_stride,
+                        void *k_out, int64_t k_out_stride, bool bf16, cudaStream_t st);
+cudaError_t launch_blocks_extend(const int32_t *new_lens, int32_t *context_lens, int32_t *pages_held,
+                                 int32_t *block_table, const int32_t *free_pages, int64_t free_capacity,
+                                 int32_t *free_count, int B, int max_pages, int64_t num_pages, int ps,
+                                 int64_t max_tokens, int32_t *token_start, int32_t *seq_ids, int32_t *positions,
+                                 int64_t *slots, uint32_t *status, cudaStream_t st);
+cudaError_t launch_blocks_trim(const int32_t *keep_lens, int32_t *context_lens, int32_t *pages_held,
+                               int32_t *block_table, int32_t *free_pages, int64_t free_capacity, int32_t *free_count,
+                               int B, int max_pages, int64_t num_pages, int ps, uint32_t *status, cudaStream_t st);
+cudaError_t launch_cache_compact(const int32_t *block_table, const int32_t *context_lens, const int32_t *token_start,
+                                 const int32_t *path, const int32_t *accept_len, int B, int64_t N, int max_path,
+                                 int max_pages, int64_t num_pages, int ps, int d_I, int d, void *kidx_cache,
+                                 float *kscale_cache, void *k_cache, float *k_scale, void *v_cache, float *v_scale,
+                                 int32_t *keep_lens, uint32_t *status, cudaStream_t st);
+// Workspace: a header, then partial results of the items that two or more CTAs share.
+size_t tree_attn_ws_bytes(int d);
+// FP8 caches where ks and vs are given.
+cudaError_t launch_tree_attn(const uint16_t *q, const void *k, const float *ks, const void *v, const float *vs,
+                             const int32_t *block_table, const int32_t *context_lens, const int32_t *token_start,
+                             const int32_t *parents, int64_t num_pages, int max_pages, int page_size, int B, int64_t N,
+                             int max_tree, int64_t max_context, int H, int Hkv, int d, float sm_scale, uint16_t *out,
+                             float *lse, void *ws, cudaStream_t st);
+cudaError_t launch_verify_tree(const float *target, const float *draft, const int32_t *tokens, const int32_t *parents,
+                               const int32_t *token_start, const float *u_accept, const float *u_sample, int B,
+                               int64_t N, int64_t V, int max_path, int32_t *path, int32_t *accept_len,
+                               int32_t *next_token, uint32_t *status, cudaStream_t st);
+
 }  // namespace dsa

@@ -1,0 +1,1110 @@
+// Attention of drafted token trees over the paged K/V caches, on the
+// 5th-generation tensor cores (tcgen05).
+//
+//   out[t,h] = sum_s softmax_s(sm q[t,h].K[s]) V[s],  s in prefix, ancestors, self
+//
+// Every drafted token of a sequence reads the same prefix, so the tokens times the
+// query heads of one K/V head are the rows of one product: tiles of 128 rows (the
+// UMMA M), two at a time where there are more than 128, against blocks of 128 cache
+// rows.  With few rows (n H_q / H_kv below about 130 for bf16) the cache's bytes bound
+// the kernel, with many the tensor pipe and the exponentials, which take as long: 128 x 128
+// exponentials at 16 a clock are 1024 clocks, the two products of a block at head
+// dim 128 also 1024.
+//
+// The work of a launch is one list: sequence by sequence, K/V head by head, pair of
+// row tiles by pair, its blocks of cache rows.  A block costs 2 for a pair of tiles and
+// 1 for a single one, and each CTA (one per SM) takes an equal share of the list,
+// wherever it begins and ends: no length or batch leaves SMs idle, and a single long
+// sequence spreads over all of them.  An item (row tiles of one sequence and head) that
+// is cut leaves partial results (fp32 O / l and log-sum-exp), which a second, chained kernel
+// merges; the others are written at once.
+//
+// Roles of a CTA (first warpgroup), bf16:
+//   warp 0  brings Q and the K and V tiles by TMA through the page table, one box
+//           of gcd(page_size, 128) rows a page, into a ring of 32 KB slots; boxes behind the
+//           context (and pages out of range) start behind the cache's last row, which
+//           TMA fills with zeros;
+//   warp 1  issues S_x = Q_x K^T into TMEM, x = 0, 1;
+//   warp 2  issues O_x += P_x V, P_x from TMEM;
+//   warp 3  walks the tree and leaves each token's ancestors as 128 bits.
+// With FP8 caches a fourth warpgroup widens the E4M3 codes to bf16 (exactly) into the
+// ring; the scales stay in fp32 and multiply the logits and the weights.
+//   warpgroups 1 and 2 are softmax sets, a thread a row: set x takes tile x of
+//           a pair, or every other block of a single tile (merged at the end).  P
+//           takes the place of S in TMEM, so a set alternates with its own MMAs while the
+//           other set's run.  O is rescaled only where the maximum grows by more
+//           than 2^8, which is exact up to rounding.
+// Every mbarrier wait is bounded (DSA_ERR_TIMEOUT on expiry).
+#include <algorithm>
+#include <numeric>
+
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int TA_M = 128;              // rows of a tile
+constexpr int TA_BLK = 128;            // cache rows of a block
+constexpr int TA_MAX_CTAS = 160;       // CTAs a workspace has room for (148 SMs)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.f;   // log2 units
+
+// Register splits: they add up to the launch's registers only for kernels built with
+// exactly these counts (checked by the build and before every launch).
+constexpr int TA_THREADS = 384, TA_REGS = 168, TA_REGS_LOW = 96, TA_REGS_HIGH = 200;
+constexpr int TA8_THREADS = 512, TA8_REGS = 128, TA8_REGS_LOW = 56, TA8_REGS_HIGH = 200;
+static_assert(128 * TA_REGS_LOW + 256 * TA_REGS_HIGH <= TA_THREADS * TA_REGS, "register split");
+static_assert(256 * TA8_REGS_LOW + 256 * TA8_REGS_HIGH <= TA8_THREADS * TA8_REGS, "register split");
+
+struct TreeArgs {
+    const uint16_t *q;
+    const int32_t *block_table, *context_lens, *token_start, *parents;
+    const float *ks, *vs;              // KV8: scales
+    int64_t num_pages, N, max_context;
+    int max_pages, page_size, box;     // box: cache rows of one TMA box
+    int B, max_tree, H, Hkv;
+    int group;                         // query heads of a K/V head
+    int rows_tok;                      // rows of a tile that one token takes: min(group, 128)
+    int tile_tok;                      // tokens of a tile (1 when group > 128)
+    int head_tiles;                    // tiles of one token (1 when group <= 128)
+    float scale_log2;
+    uint16_t *out;
+    float *lse;
+    int4 *desc;                        // [CTAs] first item of each CTA: sequence, head, tile, bits (1: cut, 2: pair)
+    uint32_t *err;                     // [CTAs] dsa_status
+    float *part;                       // [2 CTAs][256][d] O / l
+    float *part_lse;                   // [2 CTAs][256] log2 sum
+    WsHeader *hdr;
+};
+
+// Shared memory (byte offsets; the dynamic block starts on a 1024-byte boundary).
+template <bool KV8, int D> struct Smem {
+    static constexpr int halves = D / 64;
+    static constexpr int half = 128 * 128;                     // 64 columns of 128 rows
+    static constexpr int tile = halves * half;                 // one bf16 tile
+    static constexpr int slots = KV8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 10);
+    static constexpr int codes = KV8 ? (D == 128 ? 3 : 6) : 0; // KV8: staged E4M3 tiles
+    static constexpr int code_tile = 128 * D;
+    static constexpr int q_off = 0;                            // two tiles
+    // The (m, l) of both sets lie in Q's second tile, which a single tile leaves free; the
+    // next pair's Q waits until they are read.
+    static constexpr int ml_off = q_off + tile;                // [set][m, l][128]
+    static constexpr int kv_off = q_off + 2 * tile;
+    static constexpr int code_off = kv_off + slots * tile;
+    static constexpr int scale_off = code_off + codes * code_tile;       // KV8: [block % 4][K, V][128]
+    static constexpr int mask_off = scale_off + (KV8 ? 4 * 2 * 128 * 4 : 0);
+    static constexpr int parent_off = mask_off + DSA_MAX_TREE * 16;
+    static constexpr int bar_off = parent_off + DSA_MAX_TREE * 2;
+    static constexpr int n_bars = 2 + 2 * slots + 6 + 3 + 2 * codes;
+    static constexpr int ctl_off = bar_off + 8 * n_bars;
+    static constexpr int total = ctl_off + 240;
+};
+static_assert(Smem<false, 128>::total <= 232448 && Smem<false, 64>::total <= 232448, "shared memory of a CTA");
+static_assert(Smem<true, 128>::total <= 232448 && Smem<true, 64>::total <= 232448, "shared memory of a CTA");
+
+// Control words of a CTA.
+struct Ctl {
+    uint32_t tmem;
+    volatile int abort;
+    int err;                           // dsa_status
+    int start_b;                       // sequence of the CTA's first unit of work, -1: none
+    long long start_base;              // work before that sequence
+    long long c0, c1;                  // the CTA's share of the work
+    int kv_issued, q_issued, code_issued, s_issued[2], pv_issued[2];
+    long long sums[16];
+};
+static_assert(sizeof(Ctl) <= 240, "control words");
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// 2^x by the SFU (2 ulp; results below 2^-126 flush to zero, which a sum that holds a term near 1 does not notice).
+__device__ __forceinline__ float ex2_sfu(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Sixteen E4M3 codes as eight bf16 pairs, exactly.
+__device__ __forceinline__ void e4m3x16_to_bf16(const uint4 &raw, uint32_t (&out)[8])
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+        out[i] = pack_bf16x2(f.x, f.y);
+    }
+}
+
+// A sequence's tokens and context.  Returns its row tiles per K/V head x blocks of cache
+// rows (0: nothing to do), and reports what it may not be.
+struct Seq {
+    int n, ctx, tok0, tiles, nblk;
+    __device__ __forceinline__ int64_t load(const TreeArgs &a, int b, bool &bad)
+    {
+        const int64_t t0 = a.token_start[b], t1 = a.token_start[b + 1];
+        const int64_t c = a.context_lens[b], m = t1 - t0;
+        bad = false;
+        n = 0;
+        if (m == 0) return 0;
+        const int64_t room = min(a.max_context, (int64_t)a.max_pages * a.page_size);
+        if (t0 < 0 || m < 0 || t1 > a.N || m > a.max_tree || c < m || c > room) {
+            bad = true;
+            return 0;
+        }
+        n = (int)m;
+        ctx = (int)c;
+        tok0 = (int)t0;
+        tiles = a.head_tiles > 1 ? n * a.head_tiles : (n + a.tile_tok - 1) / a.tile_tok;
+        nblk = (ctx + TA_BLK - 1) / TA_BLK;
+        return (int64_t)tiles * nblk;
+    }
+};
+
+// The CTA's part of one item: blocks [blk0, blk1) for row tile `tile` (and the next, if `pair`).
+struct Segment {
+    int b, hk, tile, blk0, blk1;
+    bool pair;
+};
+
+// Walks the CTA's share [c0, c1) of the list of work.  Every role walks it for itself.
+struct Walker {
+    const TreeArgs &a;
+    int64_t c0, c1, item;              // item: work before the current item
+    Seq s;
+    int b, hk, rg;                     // rg: pair of row tiles
+    __device__ __forceinline__ Walker(const TreeArgs &args, const Ctl *ctl) : a(args)
+    {
+        c0 = ctl->c0;
+        c1 = ctl->c1;
+        b = ctl->start_b;
+        item = ctl->start_base;
+        hk = rg = 0;
+        if (b < 0) {
+            b = a.B;
+            return;
+        }
+        bool bad;
+        const int64_t per_head = s.load(a, b, bad);    // work of a K/V head
+        const int64_t rel = c0 - item;
+        hk = (int)(rel / per_head);
+        item += hk * per_head;
+        rg = (int)min((rel - hk * per_head) / (2 * s.nblk), (int64_t)(s.tiles - 1) / 2);
+        item += (int64_t)rg * 2 * s.nblk;
+    }
+    __device__ __forceinline__ bool next(Segment &g)
+    {
+        while (true) {
+            if (b >= a.B || item >= c1) return false;
+            if (s.n == 0 || hk == a.Hkv) {
+                if (++b >= a.B) return false;
+                bool bad;
+                s.load(a, b, bad);
+                hk = rg = 0;
+                continue;
+            }
+            const int w = 2 * rg + 1 < s.tiles ? 2 : 1;
+            const int64_t cost = (int64_t)w * s.nblk;
+            const int64_t lo = max(c0 - item, (int64_t)0), hi = min(c1 - item, cost);
+            g.b = b;
+            g.hk = hk;
+            g.tile = 2 * rg;
+            g.pair = w == 2;
+            g.blk0 = (int)((lo + w - 1) / w);
+            g.blk1 = (int)((hi + w - 1) / w);
+            item += cost;
+            if (2 * ++rg >= s.tiles) {
+                rg = 0;
+                ++hk;
+            }
+            if (g.blk0 < g.blk1) return true;
+        }
+    }
+};
+
+// Cache row of position p, or the row behind the last one (TMA fills it with zeros).
+__device__ __forceinline__ int cache_row(const TreeArgs &a, int b, int ctx, int p, Ctl *ctl)
+{
+    const int64_t rows = a.num_pages * a.page_size;
+    if (p >= ctx) return (int)rows;
+    const int page = a.block_table[(int64_t)b * a.max_pages + p / a.page_size];
+    if (page < 0 || page >= a.num_pages) {
+        ctl->err = DSA_ERR_INVALID_ARG;
+        return (int)rows;
+    }
+    return page * a.page_size + p % a.page_size;
+}
+
+// Four columns of a TMEM row: 128 fp32.
+__device__ __forceinline__ void tmem_row128(uint32_t taddr, uint32_t (&v)[4][32])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(taddr + c * 32, v[c]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_wait_ld_dep32(v[c]);
+}
+
+template <bool KV8, int D>
+__device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                               const CUtensorMap &vmap, const TreeArgs &a)
+{
+    using S = Smem<KV8, D>;
+    constexpr int SLOTS = S::slots, CODES = KV8 ? S::codes : 1;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::bar_off);
+    uint64_t *qfull = bars, *qempty = bars + 1, *kvfull = bars + 2, *kvempty = kvfull + SLOTS;
+    uint64_t *sfull = kvempty + SLOTS, *pfull = sfull + 2, *pvdone = pfull + 2, *oempty = pvdone + 2;
+    uint64_t *mfull = oempty + 1, *mempty = mfull + 1, *cfull = mempty + 1, *cempty = cfull + CODES;
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::ctl_off);
+    uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask_off);
+    int16_t *par = reinterpret_cast<int16_t *>(smem + S::parent_off);
+    float *scales = reinterpret_cast<float *>(smem + S::scale_off);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int threads = blockDim.x;
+
+    if (warp == 0) {
+        tmem_alloc(&ctl->tmem, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
+        for (int i = 0; i < SLOTS; ++i) { mbar_init(&kvfull[i], KV8 ? 4 : 1); mbar_init(&kvempty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&sfull[i], 1); mbar_init(&pfull[i], 4); mbar_init(&pvdone[i], 1); }
+        mbar_init(oempty, 8);
+        mbar_init(mfull, 1);
+        mbar_init(mempty, 8);
+        if (KV8)
+            for (int i = 0; i < CODES; ++i) { mbar_init(&cfull[i], 1); mbar_init(&cempty[i], 4); }
+        ctl->abort = 0;
+        ctl->err = DSA_OK;
+        ctl->start_b = -1;
+        ctl->kv_issued = ctl->q_issued = ctl->code_issued = 0;
+        ctl->s_issued[0] = ctl->s_issued[1] = ctl->pv_issued[0] = ctl->pv_issued[1] = 0;
+        fence_mbar_init();
+    }
+
+    // ---- the CTA's share of the work: a sum over the sequences, then a search
+    int64_t all = 0, mine = 0;
+    bool any_bad = false;
+    for (int b = tid; b < a.B; b += threads) {
+        Seq s;
+        bool bad;
+        const int64_t c = s.load(a, b, bad) * a.Hkv;
+        if (b == tid) mine = c;
+        all += c;
+        any_bad |= bad;
+    }
+    {
+        int64_t v = all;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) ctl->sums[warp] = v;
+    }
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < threads / 32; ++w) all += ctl->sums[w];
+    // at least two blocks a CTA: shorter shares cost more to merge than they save
+    const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, all / 2));
+    const bool works = (int64_t)blockIdx.x < ctas && all > 0;
+    const int64_t c0 = works ? all * blockIdx.x / ctas : 0, c1 = works ? all * (blockIdx.x + 1) / ctas : 0;
+    if (blockIdx.x == 0 && any_bad) ctl->err = DSA_ERR_INVALID_ARG;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B && works; b0 += threads) {
+        const int b = b0 + tid;
+        int64_t c = mine;
+        if (b0 > 0) {
+            Seq s;
+            bool bad;
+            c = b < a.B ? s.load(a, b, bad) * a.Hkv : 0;
+        }
+        int64_t v = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+        }
+        __syncthreads();
+        if (lane == 31) ctl->sums[warp] = v;
+        __syncthreads();
+        int64_t total = 0;
+        for (int w = 0; w < threads / 32; ++w) {
+            if (w < warp) v += ctl->sums[w];
+            total += ctl->sums[w];
+        }
+        const int64_t base = before + v - c;
+        if (c > 0 && base <= c0 && c0 < base + c) {
+            ctl->start_b = b;
+            ctl->start_base = base;
+        }
+        before += total;
+        if (before > c0) break;        // the same in every thread
+    }
+    if (tid == 0) {
+        ctl->c0 = c0;
+        ctl->c1 = c1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const uint32_t tS = tmem, tO = tmem + 256;     // S_x (and P_x in its first 64 columns), O_x
+
+    if (warp < 4 || warp >= 12) {
+        regs_dec<KV8 ? TA8_REGS_LOW : TA_REGS_LOW>();
+        if (warp == 0) {
+            // ------------------------------------------------ Q, K and V by TMA
+            Walker w(a, ctl);
+            Segment g;
+            const int nbox = TA_BLK / a.box;
+            const int halves = KV8 ? 1 : S::halves;
+            const int box = lane % nbox, half = lane / nbox;
+            const bool loads = half < halves;
+            uint32_t t = 0;                        // tiles issued
+            int item = 0;
+            bool was_single = false, ok = true;
+            if (lane == 0) {
+                tma_prefetch_desc(&qmap);
+                tma_prefetch_desc(&kmap);
+                tma_prefetch_desc(&vmap);
+                int4 d = make_int4(-1, 0, 0, 0);
+                Walker w0(a, ctl);
+                Segment f;
+                if (w0.next(f)) d = make_int4(f.b, f.hk, f.tile, (f.blk0 > 0 ? 1 : 0) | (f.pair ? 2 : 0));
+                a.desc[blockIdx.x] = d;
+            }
+            __syncwarp();
+            for (; ok && w.next(g); ++item) {
+                const Seq s = w.s;
+                int row = cache_row(a, g.b, s.ctx, g.blk0 * TA_BLK + box * a.box, ctl);
+                if (lane == 0) {
+                    ok = wait_or_abort(qempty, (item & 1) ^ 1, &ctl->abort);
+                    // every item's end is waited for in turn (a parity tells two phases apart, not
+                    // three); the last item's only where its (m, l) lie in the second tile's place
+                    if (ok && item >= 2) ok = wait_or_abort(oempty, item & 1, &ctl->abort);
+                    if (ok && g.pair && was_single) ok = wait_or_abort(oempty, (item & 1) ^ 1, &ctl->abort);
+                    if (ok) {
+                        const int tiles = g.pair ? 2 : 1;
+                        const int bytes = a.tile_tok * a.rows_tok * 128 * S::halves;
+                        mbar_arrive_expect_tx(qfull, tiles * bytes);
+                        ctl->q_issued = item + 1;
+                        for (int x = 0; x < tiles; ++x) {
+                            const int tl = g.tile + x;
+                            const int tok = a.head_tiles > 1 ? tl / a.head_tiles : tl * a.tile_tok;
+                            const int head = a.head_tiles > 1 ? (tl % a.head_tiles) * TA_M : 0;
+                            for (int h = 0; h < S::halves; ++h)
+                                tma_load_4d(smem + S::q_off + x * S::tile + h * S::half, &qmap, qfull, h * 64, head, g.hk,
+                                            s.tok0 + tok);
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                was_single = !g.pair;
+                for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
+                    const int here = row;
+                    if (blk + 1 < g.blk1) row = cache_row(a, g.b, s.ctx, (blk + 1) * TA_BLK + box * a.box, ctl);
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++t) {
+                        const int st = KV8 ? t % CODES : t % SLOTS;
+                        const uint32_t ph = KV8 ? t / CODES : t / SLOTS;
+                        ok = wait_or_abort(KV8 ? &cempty[st] : &kvempty[st], (ph & 1) ^ 1, &ctl->abort);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        uint64_t *full = KV8 ? &cfull[st] : &kvfull[st];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, KV8 ? S::code_tile : S::tile);
+                            if (KV8) ctl->code_issued = (int)t + 1; else ctl->kv_issued = (int)t + 1;
+                        }
+                        __syncwarp();
+                        if (loads) {
+                            uint8_t *dst = KV8 ? smem + S::code_off + st * S::code_tile + box * a.box * D
+                                               : smem + S::kv_off + st * S::tile + half * S::half + box * a.box * 128;
+                            tma_load_3d(dst, kv ? &vmap : &kmap, full, half * 64, g.hk, here);
+                        }
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ S_x = Q_x K^T
+            if (lane == 0) {
+                constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, TA_BLK, false);
+                Walker w(a, ctl);
+                Segment g;
+                uint32_t i = 0, cnt[2] = {0, 0};   // blocks; products of each set
+                int item = 0;
+                bool ok = true;
+                for (; ok && w.next(g); ++item) {
+                    ok = wait_or_abort(qfull, item & 1, &ctl->abort);
+                    for (int blk = g.blk0; ok && blk < g.blk1; ++blk, ++i) {
+                        const uint32_t t = 2 * i, st = t % SLOTS;
+                        ok = wait_or_abort(&kvfull[st], (t / SLOTS) & 1, &ctl->abort);
+                        const uint32_t ka = smem_u32(smem + S::kv_off + st * S::tile);
+                        const int x0 = g.pair ? 0 : (blk - g.blk0) & 1, x1 = g.pair ? 1 : x0;
+                        for (int x = x0; ok && x <= x1; ++x) {
+                            // P_x lies in S_x: the last P V of the set must have read it
+                            ok = wait_or_abort(&pvdone[x], (cnt[x] & 1) ^ 1, &ctl->abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t qa = smem_u32(smem + S::q_off + (g.pair ? x : 0) * S::tile);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                umma_f16(tS + x * 128, umma_desc_k_sw128(qa + (kk >> 2) * S::half + (kk & 3) * 32),
+                                         umma_desc_k_sw128(ka + (kk >> 2) * S::half + (kk & 3) * 32), idesc,
+                                         kk > 0 ? 1u : 0u);
+                            umma_commit(&sfull[x]);
+                            ctl->s_issued[x] = (int)++cnt[x];
+                        }
+                        if (ok) umma_commit(&kvempty[st]);
+                    }
+                    if (ok) umma_commit(qempty);
+                }
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------ O_x += P_x V
+            if (lane == 0) {
+                constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, D, true);
+                Walker w(a, ctl);
+                Segment g;
+                uint32_t i = 0, cnt[2] = {0, 0};
+                int item = 0;
+                bool ok = true;
+                for (; ok && w.next(g); ++item) {
+                    // the item before has read its O
+                    ok = wait_or_abort(oempty, (item & 1) ^ 1, &ctl->abort);
+                    for (int blk = g.blk0; ok && blk < g.blk1; ++blk, ++i) {
+                        const uint32_t t = 2 * i + 1, st = t % SLOTS;
+                        ok = wait_or_abort(&kvfull[st], (t / SLOTS) & 1, &ctl->abort);
+                        const uint32_t va = smem_u32(smem + S::kv_off + st * S::tile);
+                        const int x0 = g.pair ? 0 : (blk - g.blk0) & 1, x1 = g.pair ? 1 : x0;
+                        const bool first = g.pair ? blk == g.blk0 : blk - g.blk0 < 2;
+                        for (int x = x0; ok && x <= x1; ++x) {
+                            ok = wait_or_abort(&pfull[x], cnt[x] & 1, &ctl->abort);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < TA_BLK / 16; ++kk)
+                                umma_f16_ts(tO + x * 128, tS + x * 128 + kk * 8,
+                                            umma_desc_mn_sw128(va + kk * 2048, S::half, 1024), idesc,
+                                            (first && kk == 0) ? 0u : 1u);
+                            umma_commit(&pvdone[x]);
+                            ctl->pv_issued[x] = (int)++cnt[x];
+                        }
+                        if (ok) umma_commit(&kvempty[st]);
+                    }
+                }
+            }
+        } else if (warp == 3) {
+            // ------------------------------------------------ ancestors of each token
+            // Bit j of token i: j is i or above it.  0 for a padding row (and under one).
+            Walker w(a, ctl);
+            Segment g;
+            int cur = -1, seq = 0;
+            bool ok = true;
+            while (ok && w.next(g)) {
+                if (g.b == cur) continue;
+                cur = g.b;
+                const Seq s = w.s;
+                int p[DSA_MAX_TREE / 32];
+#pragma unroll
+                for (int j = 0; j < DSA_MAX_TREE / 32; ++j) {
+                    const int i = j * 32 + lane;
+                    p[j] = i < s.n ? a.parents[s.tok0 + i] : -2;
+                    if (i < s.n && p[j] >= i) {
+                        p[j] = -2;
+                        ctl->err = DSA_ERR_INVALID_ARG;
+                    }
+                    p[j] = max(p[j], -2);
+                }
+                ok = __all_sync(0xffffffffu, wait_or_abort(mempty, (seq & 1) ^ 1, &ctl->abort));
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < DSA_MAX_TREE / 32; ++j) par[j * 32 + lane] = (int16_t)p[j];
+                __syncwarp();
+                for (int i = lane; i < s.n; i += 32) {
+                    uint32_t m[4] = {0u, 0u, 0u, 0u};
+                    int j = par[i] == -2 ? -2 : i;
+                    while (j >= 0) {               // parents come before their children: at most i steps
+                        m[0] |= j < 32 ? 1u << j : 0u;
+                        m[1] |= (j >> 5) == 1 ? 1u << (j & 31) : 0u;
+                        m[2] |= (j >> 5) == 2 ? 1u << (j & 31) : 0u;
+                        m[3] |= (j >> 5) == 3 ? 1u << (j & 31) : 0u;
+                        j = par[j];
+                    }
+                    if (j == -2) m[0] = m[1] = m[2] = m[3] = 0u;
+                    *reinterpret_cast<uint4 *>(masks + 4 * i) = make_uint4(m[0], m[1], m[2], m[3]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(mfull);
+                ++seq;
+            }
+        } else if (KV8) {
+            // ------------------------------------------------ E4M3 -> bf16 (warps 12-15)
+            // Every E4M3 value is a bf16 value.  Thread i brings the two scales of
+            // row i of a block, a block ahead (their addresses go through the page table).
+            const int ct = tid - 384;
+            Walker w(a, ctl);
+            Segment g;
+            uint32_t t = 0, i = 0;
+            bool ok = true;
+            while (ok && w.next(g)) {
+                const Seq s = w.s;
+                const int64_t none = a.num_pages * a.page_size;
+                auto row_of = [&](int blk) -> int64_t {
+                    return blk < g.blk1 ? cache_row(a, g.b, s.ctx, blk * TA_BLK + ct, ctl) : none;
+                };
+                auto scale_of = [&](const float *p, int64_t r) { return r < none ? p[r * a.Hkv + g.hk] : 0.f; };
+                int64_t r1 = row_of(g.blk0);
+                float ksc = scale_of(a.ks, r1), vsc = scale_of(a.vs, r1);
+                r1 = row_of(g.blk0 + 1);
+                for (int blk = g.blk0; ok && blk < g.blk1; ++blk, ++i) {
+                    const float k_now = ksc, v_now = vsc;
+                    ksc = scale_of(a.ks, r1);
+                    vsc = scale_of(a.vs, r1);
+                    r1 = row_of(blk + 2);
+                    for (int kv = 0; kv < 2; ++kv, ++t) {
+                        const uint32_t cs = t % CODES, st = t % SLOTS;
+                        ok = wait_or_abort(&cfull[cs], (t / CODES) & 1, &ctl->abort) &&
+                             wait_or_abort(&kvempty[st], ((t / SLOTS) & 1) ^ 1, &ctl->abort);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        scales[(i & 3) * 256 + kv * 128 + ct] = kv ? v_now : k_now;
+                        const uint8_t *src = smem + S::code_off + cs * S::code_tile;
+                        uint8_t *dst = smem + S::kv_off + st * S::tile;
+#pragma unroll 4
+                        for (int j = 0; j < D / 16; ++j) {
+                            const int q = ct + 128 * j, row = q / (D / 16), c = q % (D / 16);
+                            uint4 raw = *reinterpret_cast<const uint4 *>(src + (q << 4));
+                            // rows behind the context count as zeros, whatever they hold
+                            if (blk * TA_BLK + row >= s.ctx) raw = make_uint4(0u, 0u, 0u, 0u);
+                            uint32_t o[8];
+                            e4m3x16_to_bf16(raw, o);
+                            uint8_t *p = dst + (c >> 2) * S::half + row * 128;
+                            const int c0 = (c & 3) * 2;
+                            // the two halves of a row start on the same banks: the upper one's threads
+                            // write their chunks in the other order
+                            const int f = c >> 2;
+                            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                            *reinterpret_cast<uint4 *>(p + (((c0 + f) ^ (row & 7)) << 4)) = f ? hi : lo;
+                            *reinterpret_cast<uint4 *>(p + (((c0 + 1 - f) ^ (row & 7)) << 4)) = f ? lo : hi;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&kvfull[st]);
+                            mbar_arrive(&cempty[cs]);
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        regs_inc<KV8 ? TA8_REGS_HIGH : TA_REGS_HIGH>();
+        // ------------------------------------------------ softmax sets
+        const int x = (warp >> 2) - 1;             // warps 4-7: set 0, 8-11: set 1
+        const int r = tid & 127;                   // row of the tile
+        const uint32_t trow = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tSx = tS + x * 128 + trow, tOx = tO + x * 128 + trow;
+        float *ml = reinterpret_cast<float *>(smem + S::ml_off);
+        const int tr = r / a.rows_tok, hr = r - tr * a.rows_tok;
+        Walker w(a, ctl);
+        Segment g;
+        uint32_t cnt[2] = {0, 0}, i0 = 0;          // products of each set; blocks before this segment
+        int cur = -1, seqs = 0;                    // sequence, and how many before it
+        bool masked = false;                       // its masks are there
+        bool dead = false;
+        auto need_masks = [&]() {
+            if (masked || dead) return;
+            if (!__all_sync(0xffffffffu, wait_or_abort(mfull, seqs & 1, &ctl->abort))) dead = true;
+            masked = true;
+        };
+        auto leave = [&]() {                       // the masks may be overwritten
+            if (cur < 0) return;
+            need_masks();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(mempty);
+            ++seqs;
+            masked = false;
+        };
+        while (w.next(g)) {
+            if (g.b != cur) {
+                leave();
+                cur = g.b;
+            }
+            const Seq s = w.s;
+            const int prefix = s.ctx - s.n;
+            const int tile = g.tile + (g.pair ? x : 0);
+            const int tok = (a.head_tiles > 1 ? tile / a.head_tiles : tile * a.tile_tok) + tr;
+            const int head = (a.head_tiles > 1 ? (tile % a.head_tiles) * TA_M : 0) + hr;
+            const bool valid = tr < a.tile_tok && tok < s.n && head < a.group;
+            const int node = valid ? tok : 0;
+            const int nb = g.blk1 - g.blk0;
+            const int step = g.pair ? 1 : 2, b_first = g.pair ? g.blk0 : g.blk0 + x;
+            float m = -INFINITY, l = 0.f;
+            uint32_t k = cnt[x];
+            for (int blk = b_first; blk < g.blk1 && !dead; blk += step, ++k) {
+                const uint32_t i = i0 + (blk - g.blk0), tv = 2 * i + 1, stv = tv % SLOTS;
+                bool ok = wait_or_abort(&sfull[x], k & 1, &ctl->abort);
+                // V's tile (and the scales of K and V with it)
+                const bool tail = (blk + 1) * TA_BLK > s.ctx;
+                if (KV8 || tail) ok = ok && wait_or_abort(&kvfull[stv], (tv / SLOTS) & 1, &ctl->abort);
+                if (!__all_sync(0xffffffffu, ok)) { dead = true; break; }
+                tc_fence_after();
+                uint32_t v[4][32];
+                tmem_row128(tSx, v);
+                if (KV8) {
+                    const float4 *sc = reinterpret_cast<const float4 *>(scales + (i & 3) * 256);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float4 f = sc[c];
+                        uint32_t *u = &v[c >> 3][(c & 7) * 4];
+                        u[0] = __float_as_uint(__uint_as_float(u[0]) * f.x);
+                        u[1] = __float_as_uint(__uint_as_float(u[1]) * f.y);
+                        u[2] = __float_as_uint(__uint_as_float(u[2]) * f.z);
+                        u[3] = __float_as_uint(__uint_as_float(u[3]) * f.w);
+                    }
+                }
+                if ((blk + 1) * TA_BLK > prefix) {
+                    // the drafts (and what lies behind them): column c is draft j = blk 128 + c - prefix
+                    need_masks();
+                    if (dead) break;
+                    const uint32_t *mw = masks + 4 * node;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int j0 = blk * TA_BLK + c * 32 - prefix;
+                        uint32_t bits;
+                        if (j0 <= -32) bits = 0xffffffffu;
+                        else if (j0 < 0) bits = (mw[0] << -j0) | ((1u << -j0) - 1u);
+                        else if (j0 >= DSA_MAX_TREE) bits = 0u;
+                        else bits = __funnelshift_r(mw[j0 >> 5], j0 + 32 < DSA_MAX_TREE ? mw[(j0 >> 5) + 1] : 0u, j0 & 31);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if (!((bits >> q) & 1u)) v[c][q] = 0xff800000u;
+                    }
+                    if (!KV8 && tail) {
+                        // V's rows behind the context, up to the end of their box, may hold anything:
+                        // their weights are 0, but 0 times an infinity is not
+                        const int lo = s.ctx - blk * TA_BLK, hi = (lo + a.box - 1) / a.box * a.box;
+                        uint8_t *vt = smem + S::kv_off + stv * S::tile;
+                        for (int q = r; q < (hi - lo) * S::halves * 8; q += 128) {
+                            const int row = lo + q / (S::halves * 8), c = q % (S::halves * 8);
+                            *reinterpret_cast<uint4 *>(vt + (c >> 3) * S::half + row * 128 + (c & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                float mx[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) mx[q] = __uint_as_float(v[0][q]);
+#pragma unroll
+                for (int q = 8; q < 128; ++q) mx[q & 7] = fmaxf(mx[q & 7], __uint_as_float(v[q >> 5][q & 31]));
+                const float mr = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                const float mb = mr * a.scale_log2;            // the scale is positive
+                float m_new = m, alpha = 1.f;
+                if (mb > m + kRescaleThreshold || (m == -INFINITY && mb != -INFINITY)) {
+                    m_new = mb;
+                    alpha = m == -INFINITY ? 0.f : exp2f(m - m_new);
+                }
+                const float base = m_new == -INFINITY ? 0.f : m_new;
+                const bool need = blk > b_first && alpha != 1.f;
+                // tcgen05.ld/st take the whole warp; the last P V of this set is done (S waited for it)
+                if (__any_sync(0xffffffffu, need)) {
+                    const float f = need ? alpha : 1.f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tOx + c * 32, o);
+                        tmem_wait_ld_dep32(o);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                        tmem_st32(tOx + c * 32, o);
+                    }
+                }
+                const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nb2 = f2_pack(-base, -base);
+                const uint64_t one2 = f2_pack(1.f, 1.f);
+                uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+                const float4 *vs4 = reinterpret_cast<const float4 *>(scales + (i & 3) * 256 + 128);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {                  // 64 columns: 32 words of P
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        const uint32_t *u = &v[2 * c + (q >> 4)][(2 * q) & 31];
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), sc2, nb2), x0, x1);
+                        float p0 = ex2_sfu(x0), p1 = ex2_sfu(x1);
+                        rs2[q & 3] = f2_fma(f2_pack(p0, p1), one2, rs2[q & 3]);
+                        if (KV8) {
+                            const float4 f = vs4[c * 16 + (q >> 1)];
+                            p0 *= (q & 1) ? f.z : f.x;
+                            p1 *= (q & 1) ? f.w : f.y;
+                        }
+                        pk[q] = pack_bf16x2(p0, p1);           // the products' precision: one rounding of each weight
+                    }
+                    tmem_st32(tSx + c * 32, pk);
+                }
+                float rsum = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float lo, hi;
+                    f2_unpack(rs2[q], lo, hi);
+                    rsum += lo + hi;
+                }
+                l = l * alpha + rsum;
+                m = m_new;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[x]);
+            }
+            // ---- the item's end (or this CTA's part of it)
+            const int n0 = g.pair ? nb : (nb + 1) / 2, n1 = g.pair ? nb : nb / 2;
+            cnt[0] += n0;
+            cnt[1] += n1;
+            i0 += nb;
+            need_masks();
+            const uint32_t *mw = masks + 4 * node;
+            const bool lives = valid && !dead && ((mw[node >> 5] >> (node & 31)) & 1u);
+            if (!lives) l = 0.f;                   // a padding row: zeros and -inf
+            float m_o = -INFINITY, l_o = 0.f;      // the other set's part of the row
+            if (!g.pair) {
+                ml[x * 256 + r] = m;
+                ml[x * 256 + 128 + r] = l;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                m_o = ml[(x ^ 1) * 256 + r];
+                l_o = ml[(x ^ 1) * 256 + 128 + r];
+                if (!dead && x == 1 && n0 > 0 && !wait_or_abort(&pvdone[0], (cnt[0] - 1) & 1, &ctl->abort)) dead = true;
+                if (!dead && x == 0 && n1 > 0 && !wait_or_abort(&pvdone[1], (cnt[1] - 1) & 1, &ctl->abort)) dead = true;
+            }
+            if (!dead && (x == 0 ? n0 : n1) > 0 && !wait_or_abort(&pvdone[x], (cnt[x] - 1) & 1, &ctl->abort)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) {
+                __syncwarp();
+                continue;                          // outputs stay; the status word tells
+            }
+            tc_fence_after();
+            const float mt = fmaxf(l > 0.f ? m : -INFINITY, l_o > 0.f ? m_o : -INFINITY);
+            const float f_own = l > 0.f ? exp2f(m - mt) : 0.f, f_oth = l_o > 0.f ? exp2f(m_o - mt) : 0.f;
+            const float lt = l * f_own + l_o * f_oth;
+            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const float g_own = f_own * inv, g_oth = f_oth * inv;
+            const bool whole = g.blk0 == 0 && g.blk1 == s.nblk;
+            // slot 0: an item that began in an earlier CTA, 1: one that ends in a later CTA
+            const int64_t prow = ((int64_t)blockIdx.x * 2 + (g.blk0 > 0 ? 0 : 1)) * 256 + (g.pair ? x * 128 : 0) + r;
+            const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + g.hk * a.group + head;
+            // a single tile: set x takes half of the columns of both parts
+            const int col0 = g.pair ? 0 : x * (D / 2), cols = g.pair ? D : D / 2;
+            const bool have_own = (x == 0 ? n0 : n1) > 0, have_oth = !g.pair && (x == 0 ? n1 : n0) > 0;
+            const uint32_t tOo = tO + (x ^ 1) * 128 + trow;
+            for (int c = col0; c < col0 + cols; c += 32) {
+                uint32_t o[32];
+                float acc[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q) acc[q] = 0.f;
+                if (have_own) {
+                    tmem_ld32(tOx + c, o);
+                    tmem_wait_ld_dep32(o);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) acc[q] = __uint_as_float(o[q]) * g_own;
+                }
+                if (have_oth) {
+                    tmem_ld32(tOo + c, o);
+                    tmem_wait_ld_dep32(o);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) acc[q] += __uint_as_float(o[q]) * g_oth;
+                }
+                if (!lives) {
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) acc[q] = 0.f;
+                }
+                if (whole) {
+                    if (valid) {
+                        uint4 *p = reinterpret_cast<uint4 *>(a.out + orow * D + c);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            p[u] = make_uint4(pack_bf16x2(acc[8 * u], acc[8 * u + 1]), pack_bf16x2(acc[8 * u + 2], acc[8 * u + 3]),
+                                              pack_bf16x2(acc[8 * u + 4], acc[8 * u + 5]), pack_bf16x2(acc[8 * u + 6], acc[8 * u + 7]));
+                    }
+                } else if (valid) {
+                    float4 *p = reinterpret_cast<float4 *>(a.part + prow * D + c);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) p[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
+                }
+            }
+            if (valid && (g.pair || x == 0)) {
+                const float l2 = lives && lt > 0.f ? mt + log2f(lt) : -INFINITY;
+                if (!whole) a.part_lse[prow] = l2;
+                else if (a.lse) a.lse[orow] = lives && lt > 0.f ? mt * kLn2 + logf(lt) : -INFINITY;
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();              // ml, before TMA may write Q there
+            __syncwarp();
+            if (lane == 0) mbar_arrive(oempty);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+        if (ctl->abort) {
+            ctl->err = DSA_ERR_TIMEOUT;
+            // let copies and products in flight land before shared and tensor memory go
+            const int n_kv = KV8 ? ctl->code_issued : ctl->kv_issued, ring = KV8 ? CODES : SLOTS;
+            for (int j = max(0, n_kv - ring); j < n_kv; ++j)
+                mbar_wait(KV8 ? &cfull[j % ring] : &kvfull[j % ring], (j / ring) & 1);
+            if (ctl->q_issued > 0) mbar_wait(qfull, (ctl->q_issued - 1) & 1);
+            for (int y = 0; y < 2; ++y) {
+                if (ctl->s_issued[y] > 0) mbar_wait(&sfull[y], (ctl->s_issued[y] - 1) & 1);
+                if (ctl->pv_issued[y] > 0) mbar_wait(&pvdone[y], (ctl->pv_issued[y] - 1) & 1);
+            }
+        }
+        a.err[blockIdx.x] = (uint32_t)ctl->err;
+    }
+    __syncthreads();
+    tc_fence_after();
+    grid_dep_trigger();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+__global__ void __launch_bounds__(TA_THREADS, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeArgs a)
+{
+    tree_attn_body<false, D>(qmap, kmap, vmap, a);
+}
+
+template <int D>
+__global__ void __launch_bounds__(TA8_THREADS, 1)
+tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeArgs a)
+{
+    tree_attn_body<true, D>(qmap, kmap, vmap, a);
+}
+
+// ---------------------------------------------------------------- merge of cut items
+
+// Parts of a cut item: the last of the CTA where it began (slot 1), and the first
+// (slot 0) of every CTA behind it up to its end.
+//   out = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M),  L_i the parts' log2 sums.
+constexpr int TM_THREADS = 256;
+
+template <int D>
+__global__ void __launch_bounds__(TM_THREADS)
+tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
+{
+    grid_dep_wait();
+    __shared__ int4 desc[TA_MAX_CTAS];
+    __shared__ int first[TA_MAX_CTAS];         // CTAs in whose share a cut item continues for the first time
+    __shared__ int n_items;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int c = tid; c < ctas; c += TM_THREADS) desc[c] = a.desc[c];
+    if (tid == 0) n_items = 0;
+    if (blockIdx.x == 0 && warp == 0) {        // the call's status word: the worst of the CTAs'
+        uint32_t e = 0;
+        for (int c = lane; c < ctas; c += 32) e = max(e, a.err[c]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+        if (lane == 0) {
+            a.hdr->status = e;
+            a.hdr->detail = 0;
+        }
+    }
+    __syncthreads();
+    auto same = [&](int c, int d) { return desc[c].x == desc[d].x && desc[c].y == desc[d].y && desc[c].z == desc[d].z; };
+    if (warp == 0) {                           // in order
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const int c = c0 + lane;
+            const bool f = c > 0 && c < ctas && desc[c].x >= 0 && (desc[c].w & 1) && !((desc[c - 1].w & 1) && same(c, c - 1));
+            const unsigned fs = __ballot_sync(0xffffffffu, f);
+            if (f) first[n_items + __popc(fs & ((1u << lane) - 1u))] = c;
+            __syncwarp();
+            if (lane == 0) n_items += __popc(fs);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    // a warp per row: 256 rows an item
+    for (int64_t u = (int64_t)blockIdx.x * (TM_THREADS / 32) + warp; u < (int64_t)n_items * 256;
+         u += (int64_t)gridDim.x * (TM_THREADS / 32)) {
+        const int c = first[u >> 8], row = (int)(u & 255);
+        const int4 d = desc[c];
+        Seq s;
+        bool bad;
+        s.load(a, d.x, bad);
+        const int x = row >> 7, r = row & 127;
+        if (x == 1 && !(d.w & 2)) continue;
+        const int tile = d.z + x, tr = r / a.rows_tok;
+        const int tok = (a.head_tiles > 1 ? tile / a.head_tiles : tile * a.tile_tok) + tr;
+        const int head = (a.head_tiles > 1 ? (tile % a.head_tiles) * TA_M : 0) + r - tr * a.rows_tok;
+        if (tr >= a.tile_tok || tok >= s.n || head >= a.group) continue;
+        int parts = 1;
+        while (c + parts - 1 < ctas && (desc[c + parts - 1].w & 1) && same(c, c + parts - 1)) ++parts;
+        // part 0: slot 1 of CTA c - 1; part p: slot 0 of CTA c - 1 + p
+        auto at = [&](int p) -> int64_t { return ((int64_t)(c - 1 + p) * 2 + (p == 0 ? 1 : 0)) * 256 + row; };
+        float M = -INFINITY;
+        for (int p = lane; p < parts; p += 32) M = fmaxf(M, a.part_lse[at(p)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        constexpr int E = D / 32;
+        float acc[E], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        if (M != -INFINITY) {
+            for (int p0 = 0; p0 < parts; p0 += 8) {
+                float wt[8], o[8][E];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    wt[q] = 0.f;
+                    if (p0 + q >= parts) continue;
+                    wt[q] = exp2f(a.part_lse[at(p0 + q)] - M);
+                    const float *po = a.part + at(p0 + q) * D + lane * E;
+                    if (E == 4) *reinterpret_cast<float4 *>(o[q]) = *reinterpret_cast<const float4 *>(po);
+                    else *reinterpret_cast<float2 *>(o[q]) = *reinterpret_cast<const float2 *>(po);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (p0 + q >= parts) continue;
+                    sum += wt[q];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += wt[q] * o[q][e];
+                }
+            }
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + d.y * a.group + head;
+        uint32_t w2[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        if (E == 4) *reinterpret_cast<uint2 *>(a.out + orow * D + lane * E) = make_uint2(w2[0], w2[E / 2 - 1]);
+        else *reinterpret_cast<uint32_t *>(a.out + orow * D + lane * E) = w2[0];
+        if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? M * kLn2 + logf(sum) : -INFINITY;
+    }
+}
+
+template <bool KV8, int D>
+cudaError_t launch_tree_t(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const TreeArgs &a,
+                          int ctas, cudaStream_t st)
+{
+    auto kernel = KV8 ? tree_attn_kv8_kernel<D> : tree_attn_kernel<D>;
+    constexpr int smem = Smem<KV8, D>::total;
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    // the register split assumes it: an error, not a wait that never ends
+    if (fa.numRegs != (KV8 ? TA8_REGS : TA_REGS)) return cudaErrorInvalidKernelImage;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)ctas, KV8 ? TA8_THREADS : TA_THREADS, smem, st>>>(qmap, kmap, vmap, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_chained(tree_merge_kernel<D>, dim3(148 * 4), dim3(TM_THREADS), 0, st, a, ctas);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// Workspace: header, then these.
+struct TreeWs {
+    size_t desc, err, lse, part, end;
+    explicit TreeWs(int d)
+    {
+        desc = kWsHeader;
+        err = desc + sizeof(int4) * TA_MAX_CTAS;
+        lse = err + align_up(sizeof(uint32_t) * TA_MAX_CTAS, 256);
+        part = lse + sizeof(float) * 2 * 256 * TA_MAX_CTAS;
+        end = part + sizeof(float) * 2 * 256 * (size_t)d * TA_MAX_CTAS;
+    }
+};
+
+}  // namespace
+
+size_t tree_attn_ws_bytes(int d) { return TreeWs(d).end; }
+
+cudaError_t launch_tree_attn(const uint16_t *q, const void *k, const float *ks, const void *v, const float *vs,
+                             const int32_t *block_table, const int32_t *context_lens, const int32_t *token_start,
+                             const int32_t *parents, int64_t num_pages, int max_pages, int page_size, int B, int64_t N,
+                             int max_tree, int64_t max_context, int H, int Hkv, int d, float sm_scale, uint16_t *out,
+                             float *lse, void *ws, cudaStream_t st)
+{
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    const TreeWs L(d);
+    TreeArgs a{};
+    a.q = q;
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.token_start = token_start;
+    a.parents = parents;
+    a.ks = ks;
+    a.vs = vs;
+    a.num_pages = num_pages;
+    a.N = N;
+    a.max_context = max_context;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.box = std::gcd(page_size, TA_BLK);
+    a.B = B;
+    a.max_tree = max_tree;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.group = H / Hkv;
+    a.rows_tok = std::min(a.group, TA_M);
+    a.tile_tok = TA_M / a.rows_tok;
+    a.head_tiles = (int)ceil_div(a.group, TA_M);
+    a.scale_log2 = sm_scale * kLog2e;
+    a.out = out;
+    a.lse = lse;
+    a.desc = reinterpret_cast<int4 *>(w + L.desc);
+    a.err = reinterpret_cast<uint32_t *>(w + L.err);
+    a.part_lse = reinterpret_cast<float *>(w + L.lse);
+    a.part = reinterpret_cast<float *>(w + L.part);
+    a.hdr = reinterpret_cast<WsHeader *>(w);
+
+    int dev = 0, sms = 148;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // one CTA per SM, and no more than the largest possible list of work feeds
+    const int64_t tiles = a.head_tiles > 1 ? N * a.head_tiles : ceil_div(N, a.tile_tok) + B;
+    const int64_t most = tiles * Hkv * ceil_div(std::min(max_context, (int64_t)max_pages * page_size), TA_BLK);
+    const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)sms, (int64_t)TA_MAX_CTAS, ceil_div(most, 2)}));
+
+    CUtensorMap qmap, kmap, vmap;
+    const uint64_t rows = (uint64_t)num_pages * page_size;
+    const uint64_t qd[4] = {(uint64_t)d, (uint64_t)a.group, (uint64_t)Hkv, (uint64_t)N};
+    const uint64_t qs[3] = {2ull * d, 2ull * d * a.group, 2ull * d * H};
+    const uint32_t qb[4] = {64, (uint32_t)a.rows_tok, 1, (uint32_t)a.tile_tok};
+    if (!make_tmap_bf16(&qmap, q, 4, qd, qs, qb)) return cudaErrorNotSupported;
+    const uint64_t kd[3] = {(uint64_t)d, (uint64_t)Hkv, rows};
+    const uint64_t size = ks ? 1 : 2;
+    const uint64_t kst[2] = {size * d, size * d * Hkv};
+    const uint32_t kb[3] = {ks ? (uint32_t)d : 64u, 1, (uint32_t)a.box};
+    const bool maps = ks ? make_tmap_u8_linear(&kmap, k, 3, kd, kst, kb) && make_tmap_u8_linear(&vmap, v, 3, kd, kst, kb)
+                         : make_tmap_bf16(&kmap, k, 3, kd, kst, kb) && make_tmap_bf16(&vmap, v, 3, kd, kst, kb);
+    if (!maps) return cudaErrorNotSupported;
+    if (ks) return d == 128 ? launch_tree_t<true, 128>(qmap, kmap, vmap, a, ctas, st)
+                            : launch_tree_t<true, 64>(qmap, kmap, vmap, a, ctas, st);
+    return d == 128 ? launch_tree_t<false, 128>(qmap, kmap, vmap, a, ctas, st)
+                    : launch_tree_t<false, 64>(qmap, kmap, vmap, a, ctas, st);
+}
+
+}  // namespace dsa

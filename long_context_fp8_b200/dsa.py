@@ -8,6 +8,7 @@ an error status, a ``DSAError`` is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -30,7 +31,9 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_index_scores", "dsa_topk_wor
            "dsa_quantize_e4m3", "dsa_cache_append", "dsa_cache_append_kv8", "dsa_decode_noalloc",
            "dsa_split_workspace_size", "dsa_decode_select", "dsa_merge_selections", "dsa_decode_attend",
            "dsa_merge_partials", "dsa_stream_status", "dsa_profile_enable", "dsa_profile_read",
-           "dsa_prefill_rows_workspace_size", "dsa_prefill_rows", "dsa_test_stall_next")
+           "dsa_prefill_rows_workspace_size", "dsa_prefill_rows", "dsa_test_stall_next",
+           "dsa_rope_freqs", "dsa_rope", "dsa_blocks_extend", "dsa_blocks_trim", "dsa_tree_attn_workspace_size",
+           "dsa_tree_attn", "dsa_verify_tree", "dsa_cache_compact")
 
 
 class DSAError(RuntimeError):
@@ -53,6 +56,7 @@ def load(path: str = LIB_PATH):
             "`python -m long_context_fp8_b200.build`")
     lib = ctypes.CDLL(path)
     P, I64, I32, F, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    D = ctypes.c_double
     sig = {
         "dsa_status_string": ([I32], ctypes.c_char_p),
         "dsa_version": ([], I32),
@@ -97,6 +101,16 @@ def load(path: str = LIB_PATH):
         "dsa_prefill_rows": ([P, P, P, P, P, P, P, P, I64, I64, I64, I32, I32, I32, I32, I32, F, P, P, P, I32, P,
                               SZ, P], I32),
         "dsa_profile_read": ([P, P], I32),
+        "dsa_rope_freqs": ([I32, D, I32, D, I64, D, D, P], I32),
+        "dsa_rope": ([P, I64, I32, P, I64, I32, P, I64, I32, I32, I32, I32, P, F, I32, P, I64, P, I64, I32, P], I32),
+        "dsa_blocks_extend": ([P, P, P, P, P, I64, P, I32, I32, I64, I32, I64, P, P, P, P, P, P], I32),
+        "dsa_blocks_trim": ([P, P, P, P, P, I64, P, I32, I32, I64, I32, P, P], I32),
+        "dsa_tree_attn_workspace_size": ([I32, I64, I32, I32, I32], SZ),
+        "dsa_tree_attn": ([P, P, P, P, P, P, P, P, P, I64, I32, I32, I32, I64, I32, I64, I32, I32, I32, F, P, P, P,
+                           SZ, P], I32),
+        "dsa_verify_tree": ([P, P, P, P, P, P, P, I32, I64, I64, I32, P, P, P, P, P], I32),
+        "dsa_cache_compact": ([P, P, P, P, P, I32, I64, I32, I32, I64, I32, I32, I32, P, P, P, P, P, P, P, P, P],
+                              I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -591,6 +605,238 @@ def dsa_merge_partials(part_out, part_lse, out=None, lse=None, stream=None):
 def dsa_stream_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronise the stream and return (and clear) the workspace's device status."""
     return load().dsa_stream_status(_p(ws), _stream(stream))
+
+
+# ---- speculative decoding
+
+ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
+MAX_TREE = 128
+
+
+def _on(ref: torch.Tensor):
+    """Device context of a call: the tensors' device, where it is not the current one."""
+    if ref.device.index in (None, torch.cuda.current_device()):
+        return contextlib.nullcontext()
+    return torch.cuda.device(ref.device)
+
+
+def _t(t: Optional[torch.Tensor], dtype, ref: torch.Tensor, shape=None):
+    """Address of a contiguous tensor of that type (and shape) on ref's device."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"expected {dtype}, got {t.dtype}")
+    if t.device != ref.device:
+        raise ValueError(f"tensors on {t.device} and {ref.device}")
+    if not t.is_contiguous():
+        raise ValueError("DSA entry points take contiguous tensors")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _cuda(t: torch.Tensor) -> torch.Tensor:
+    if not t.is_cuda:
+        raise ValueError("DSA entry points take CUDA tensors")
+    return t
+
+
+def _raw_stream(stream, ref: torch.Tensor) -> int:
+    return torch.cuda.current_stream(ref.device).cuda_stream if stream is None else stream.cuda_stream
+
+
+def dsa_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                   original_context: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Frequency table of dsa_rope (host memory; make it once): a ctypes array
+    of rot_dim / 2 rotations per position, in 2^-64 turns."""
+    turns = (ctypes.c_uint64 * max(rot_dim // 2, 1))()
+    _check("dsa_rope_freqs", load().dsa_rope_freqs(rot_dim, base, ROPE_SCALING[scaling], factor, original_context,
+                                                   beta_fast, beta_slow, ctypes.addressof(turns)))
+    return turns
+
+
+def _rope_rows(x: torch.Tensor, like: Optional[torch.Tensor] = None) -> int:
+    """Address check of [rows, H, d] with dense heads and any row stride."""
+    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1) or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise ValueError("dsa_rope takes [rows, H, d] with dense heads")
+    if like is not None and (x.shape != like.shape or x.dtype != like.dtype or x.device != like.device):
+        raise ValueError("dsa_rope's tensors must agree in shape, type and device")
+    # a single row's stride says nothing
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def dsa_rope(q, positions, freqs, k=None, rot_begin=0, interleaved=False, attn_factor=1.0, inverse=False,
+             q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [rows, H_q, d] and k [rows, H_k, d] (bf16 or fp32,
+    rows any stride apart): 2 * len(freqs) elements of each head from
+    ``rot_begin`` on, by ``positions`` int32 [rows] and dsa_rope_freqs' table.
+    ``inverse``: the gradient of the forward call.  ``q_out is q`` rotates in
+    place.  Returns (q_out, k_out)."""
+    rows, H_q, d = _cuda(q).shape
+    dt = _val_dtype(q)
+    qs = _rope_rows(q)
+    if q_out is None:
+        q_out = torch.empty((rows, H_q, d), dtype=q.dtype, device=q.device)
+    qos = _rope_rows(q_out, q)
+    kp = kop = None
+    ks = kos = H_k = 0
+    if k is not None:
+        H_k = k.shape[1]
+        if k.shape[0] != rows or k.shape[2] != d or k.dtype != q.dtype or k.device != q.device:
+            raise ValueError("q and k must agree in rows, head dimension, type and device")
+        ks = _rope_rows(k)
+        if k_out is None:
+            k_out = torch.empty((rows, H_k, d), dtype=k.dtype, device=k.device)
+        kos = _rope_rows(k_out, k)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    with _on(q):
+        st = load().dsa_rope(q.data_ptr(), qs, H_q, kp, ks, H_k, _t(positions, torch.int32, q, (rows,)), rows, d,
+                             rot_begin, 2 * len(freqs), int(bool(interleaved)), ctypes.addressof(freqs), attn_factor,
+                             int(bool(inverse)), q_out.data_ptr(), qos, kop, kos, dt, _raw_stream(stream, q))
+    _check("dsa_rope", st)
+    return q_out, k_out
+
+
+def dsa_blocks_extend(pool: dict, new_lens, page_size: int, num_pages: int, max_tokens: int, plan=None, status=None,
+                      stream=None):
+    """Grow sequence b by new_lens[b] tokens: pages from the pool's free stack
+    into its block table.  ``pool`` (int32, updated in place): block_table
+    [B, max_pages], context_lens [B], pages_held [B], free_pages [capacity],
+    free_count [1].  Returns ``plan``: token_start [B + 1], seq_ids and
+    positions [max_tokens], slots int64 [max_tokens] (-1 behind the last
+    token).  ``status``: as in dsa_cache_append."""
+    bt = _cuda(pool["block_table"])
+    B, max_pages = bt.shape
+    i32, dev = torch.int32, bt.device
+    if plan is None:
+        plan = {"token_start": torch.empty(B + 1, dtype=i32, device=dev),
+                "seq_ids": torch.empty(max_tokens, dtype=i32, device=dev),
+                "positions": torch.empty(max_tokens, dtype=i32, device=dev),
+                "slots": torch.empty(max_tokens, dtype=torch.int64, device=dev)}
+    free = pool["free_pages"]
+    with _on(bt):
+        st = load().dsa_blocks_extend(
+            _t(new_lens, i32, bt, (B,)), _t(pool["context_lens"], i32, bt, (B,)), _t(pool["pages_held"], i32, bt, (B,)),
+            _t(bt, i32, bt), _t(free, i32, bt), free.numel(), _t(pool["free_count"], i32, bt, (1,)), B, max_pages,
+            num_pages, page_size, max_tokens, _t(plan["token_start"], i32, bt, (B + 1,)),
+            _t(plan["seq_ids"], i32, bt, (max_tokens,)), _t(plan["positions"], i32, bt, (max_tokens,)),
+            _t(plan.get("slots"), torch.int64, bt, (max_tokens,)), _t(status, i32, bt), _raw_stream(stream, bt))
+    _check("dsa_blocks_extend", st)
+    return plan
+
+
+def dsa_blocks_trim(pool: dict, keep_lens, page_size: int, num_pages: Optional[int] = None, status=None, stream=None):
+    """Cut every sequence back to keep_lens[b] tokens and give the pages behind
+    them back to the pool (as in dsa_blocks_extend).  ``num_pages`` bounds the
+    page ids (default: the largest that page_size allows)."""
+    bt = _cuda(pool["block_table"])
+    B, max_pages = bt.shape
+    i32 = torch.int32
+    free = pool["free_pages"]
+    num_pages = (2 ** 31 - 1) // page_size if num_pages is None and page_size > 0 else num_pages
+    with _on(bt):
+        st = load().dsa_blocks_trim(
+            _t(keep_lens, i32, bt, (B,)), _t(pool["context_lens"], i32, bt, (B,)), _t(pool["pages_held"], i32, bt, (B,)),
+            _t(bt, i32, bt), _t(free, i32, bt), free.numel(), _t(pool["free_count"], i32, bt, (1,)), B, max_pages,
+            num_pages, page_size, _t(status, i32, bt), _raw_stream(stream, bt))
+    _check("dsa_blocks_trim", st)
+
+
+def tree_attn_workspace_size(B, N, H_q, H_kv, d) -> int:
+    return load().dsa_tree_attn_workspace_size(B, N, H_q, H_kv, d)
+
+
+def dsa_tree_attn(inp: dict, max_tree: int, max_context: int, sm_scale=None, out=None, lse=None, ws=None, stream=None):
+    """Attention of packed drafted tokens over the paged caches -> (out, lse).
+    ``inp``: q bf16 [N, H_q, d]; k_cache, v_cache [P, page_size, H_kv, d] (or
+    [P, page_size, d]: one K/V head), bf16, or uint8 E4M3 codes with
+    k_cache_scale, v_cache_scale [P, page_size(, H_kv)]; block_table,
+    context_lens (drafts included), token_start [B + 1] and parents [N]
+    int32.  A caller that keeps the workspace (``ws``) saves its allocation."""
+    q, kc, bt = _cuda(inp["q"]), inp["k_cache"], inp["block_table"]
+    N, H_q, d = q.shape
+    P, ps = kc.shape[0], kc.shape[1]
+    H_kv = kc.shape[2] if kc.dim() == 4 else 1
+    B, max_pages = bt.shape
+    i32, f32 = torch.int32, torch.float32
+    sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
+    lib = load()
+    if ws is None:
+        ws = workspace(lib.dsa_tree_attn_workspace_size(B, N, H_q, H_kv, d), q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((N, H_q), dtype=f32, device=q.device)
+    ksc, vsc = inp.get("k_cache_scale"), inp.get("v_cache_scale")
+    if kc.shape[-1] != d:
+        raise ValueError(f"expected cache rows of {d} values, got {kc.shape[-1]}")
+    code, scale_shape = torch.bfloat16 if ksc is None else torch.uint8, kc.shape[:-1]
+    with _on(q):
+        st = lib.dsa_tree_attn(_t(q, torch.bfloat16, q), _t(kc, code, q), _t(ksc, f32, q, scale_shape),
+                               _t(inp["v_cache"], code, q, kc.shape), _t(vsc, f32, q, scale_shape), _t(bt, i32, q),
+                               _t(inp["context_lens"], i32, q, (B,)), _t(inp["token_start"], i32, q, (B + 1,)),
+                               _t(inp["parents"], i32, q, (N,)), P, max_pages, ps, B, N, max_tree, max_context, H_q,
+                               H_kv, d, sm_scale, _t(out, torch.bfloat16, q, q.shape), _t(lse, f32, q, (N, H_q)),
+                               _t(ws, torch.uint8, q), ws.numel(), _raw_stream(stream, q))
+    _check("dsa_tree_attn", st)
+    return out, lse
+
+
+def dsa_verify_tree(target_probs, draft_probs, tokens, parents, token_start, u_accept, u_sample, max_path=None,
+                    path=None, accept_len=None, next_token=None, status=None, stream=None):
+    """Verify drafted trees: target_probs and draft_probs f32 [N, V] (draft
+    None: point masses), tokens, parents int32 [N], token_start int32 [B + 1],
+    u_accept f32 [N], u_sample f32 [B] -> (path int32 [B, max_path],
+    accept_len int32 [B], next_token int32 [B]).  ``status``: as in
+    dsa_cache_append."""
+    N, V = _cuda(target_probs).shape
+    B = u_sample.shape[0]
+    i32, f32, ref = torch.int32, torch.float32, target_probs
+    if path is None:
+        path = torch.empty((B, MAX_TREE if max_path is None else max_path), dtype=i32, device=ref.device)
+    elif max_path not in (None, path.shape[1]):
+        raise ValueError("path's width is max_path")
+    if accept_len is None:
+        accept_len = torch.empty((B,), dtype=i32, device=ref.device)
+    if next_token is None:
+        next_token = torch.empty((B,), dtype=i32, device=ref.device)
+    with _on(ref):
+        st = load().dsa_verify_tree(_t(ref, f32, ref), _t(draft_probs, f32, ref, ref.shape), _t(tokens, i32, ref, (N,)),
+                                    _t(parents, i32, ref, (N,)), _t(token_start, i32, ref, (B + 1,)),
+                                    _t(u_accept, f32, ref, (N,)), _t(u_sample, f32, ref, (B,)), B, N, V, path.shape[1],
+                                    _t(path, i32, ref, (B, path.shape[1])), _t(accept_len, i32, ref, (B,)),
+                                    _t(next_token, i32, ref, (B,)), _t(status, i32, ref), _raw_stream(stream, ref))
+    _check("dsa_verify_tree", st)
+    return path, accept_len, next_token
+
+
+def dsa_cache_compact(caches: dict, block_table, context_lens, token_start, path, accept_len, N=None, keep_lens=None,
+                      status=None, stream=None):
+    """Move the accepted paths' rows together in the paged ``caches`` (updated
+    in place): k_cache, v_cache [P, page_size, d], bf16 or E4M3 codes with
+    k_cache_scale, v_cache_scale [P, page_size], and kidx_cache with
+    kscale_cache where given.  ``N`` bounds token_start (default: none).
+    Returns keep_lens int32 [B], the lengths to trim to."""
+    bt = _cuda(block_table)
+    B, max_pages = bt.shape
+    i32, f32 = torch.int32, torch.float32
+    kc, ki, ksc = caches["k_cache"], caches.get("kidx_cache"), caches.get("k_cache_scale")
+    P, ps, d = kc.shape
+    code, slots = torch.bfloat16 if ksc is None else torch.uint8, kc.shape[:2]
+    if keep_lens is None:
+        keep_lens = torch.empty((B,), dtype=i32, device=bt.device)
+    max_path = path.shape[1]
+    d_I = ki.shape[2] if ki is not None else 0
+    with _on(bt):
+        st = load().dsa_cache_compact(
+            _t(bt, i32, bt), _t(context_lens, i32, bt, (B,)), _t(token_start, i32, bt, (B + 1,)),
+            _t(path, i32, bt, (B, max_path)), _t(accept_len, i32, bt, (B,)), B, 2 ** 31 - 1 if N is None else N,
+            max_path, max_pages, P, ps, d_I, d, _t(ki, torch.uint8, bt, (P, ps, d_I)),
+            _t(caches.get("kscale_cache"), f32, bt, slots), _t(kc, code, bt), _t(ksc, f32, bt, slots),
+            _t(caches["v_cache"], code, bt, kc.shape), _t(caches.get("v_cache_scale"), f32, bt, slots),
+            _t(keep_lens, i32, bt, (B,)), _t(status, i32, bt), _raw_stream(stream, bt))
+    _check("dsa_cache_compact", st)
+    return keep_lens
 
 
 # Stage names of dsa_profile_read, in dsa_stage order.
