@@ -3,6 +3,8 @@
 nvcc compiles every ``csrc/*.cu`` for sm_100a only (``-gencode
 arch=compute_100a,code=sm_100a``) and links one shared library with the CUDA
 runtime linked statically, so the library depends on nothing but the driver.
+g++ compiles ``csrc/bind.cpp``, the Python binding of the speculative-decoding
+entry points, against the installed torch: ``long_context_fp8_b200/_bind.so``.
 Usable as ``python -m long_context_fp8_b200.build``.
 """
 from __future__ import annotations
@@ -20,6 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdsa_b200.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -95,6 +99,34 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def build_binding(verbose: bool = False) -> str:
+    """Compile the Python binding against the installed torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp, libs = BIND + ".tmp", os.path.join(root, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE]
+    for p in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", p]
+    cmd += [BIND_SRC, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl",
+            "-Wl,-rpath," + libs]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
+def binding_up_to_date() -> bool:
+    return os.path.exists(BIND) and all(
+        os.path.getmtime(p) <= os.path.getmtime(BIND) for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
@@ -103,6 +135,8 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    if force or not binding_up_to_date():
+        build_binding(verbose)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)

@@ -7,43 +7,51 @@
 // second, chained launch, 16 bytes a token at HBM rate; up to BL_SMALL tokens the
 // first block writes them itself and the second launch is saved.  At the sizes of
 // a decode step all of this is latency: two scans, one table write, one read.
+#include <cooperative_groups.h>
+
 #include "kernels.h"
 
 namespace dsa {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int BL_THREADS = 1024;
 // Tokens that the scanning block maps itself.
 constexpr int64_t BL_SMALL = 4096;
+// Blocks that share the pages out where there may be many.
+constexpr int BL_CLUSTER = 8;
 
 __device__ __forceinline__ void report(uint32_t *status, dsa_status s)
 {
     if (status) atomicCAS(status, (uint32_t)DSA_OK, (uint32_t)s);
 }
 
-// Inclusive sum over the block (BL_THREADS threads); *total gets the block's.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *warp_sums, int64_t *total)
+struct Two { int64_t a, b; };
+
+__device__ __forceinline__ Two warp_scan(Two v, int lane)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += t;
+        const int64_t a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o);
+        if (lane >= o) { v.a += a; v.b += b; }
     }
+    return v;
+}
+
+// Inclusive sums of two values over the block (BL_THREADS threads); *total gets the block's.
+__device__ __forceinline__ Two block_scan(Two v, Two *warp_sums, Two *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_scan(v, lane);
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        int64_t w = warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += t;
-        }
-        warp_sums[lane] = w;
-    }
-    __syncthreads();
-    if (warp > 0) v += warp_sums[warp - 1];
-    *total = warp_sums[31];
+    // every warp sums the warps' totals for itself: one barrier less
+    const Two w = warp_scan(warp_sums[lane], lane);
+    total->a = __shfl_sync(0xffffffffu, w.a, 31);
+    total->b = __shfl_sync(0xffffffffu, w.b, 31);
+    const int64_t ba = __shfl_sync(0xffffffffu, w.a, (warp + 31) & 31), bb = __shfl_sync(0xffffffffu, w.b, (warp + 31) & 31);
+    if (warp > 0) { v.a += ba; v.b += bb; }
     __syncthreads();                   // warp_sums may be written again
     return v;
 }
@@ -69,30 +77,36 @@ struct Maps {
     uint32_t *status;
 };
 
-// The maps of four tokens t .. t + 3 (t a multiple of 4).
-__device__ __forceinline__ void write_maps(const Maps &m, int64_t t)
+// The maps of four tokens t .. t + 3 (t a multiple of 4).  `ends` and `lens`: token_start + 1 and context_lens,
+// or copies of them.
+__device__ __forceinline__ void write_maps(const Maps &m, const int32_t *ends, const int32_t *lens, int64_t t)
 {
-    int b = upper(m.token_start + 1, m.B, t);
+    int b = upper(ends, m.B, t);
     int32_t sid[4], pos[4];
     int64_t slot[4];
     int32_t stop = 0, ctx = 0;
     int have = -1;
+    int32_t at = -1, page = -1;        // column of the table and the page there
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         sid[j] = pos[j] = -1;
         slot[j] = -1;
-        while (b < m.B && (have == b ? stop : m.token_start[b + 1]) <= t + j) ++b;
+        while (b < m.B && (have == b ? stop : ends[b]) <= t + j) ++b;
         if (b >= m.B) continue;
         if (have != b) {
-            stop = m.token_start[b + 1];
-            ctx = m.context_lens[b];   // already the new length
+            stop = ends[b];
+            ctx = lens[b];             // already the new length
             have = b;
+            at = -1;
         }
         sid[j] = b;
-        const int p = ctx - stop + (int)(t + j);
+        const int p = ctx - stop + (int)(t + j), col = p / m.ps;
         pos[j] = p;
-        const int64_t page = m.block_table[(int64_t)b * m.max_pages + p / m.ps];
-        if (page >= 0 && page < m.num_pages) slot[j] = page * m.ps + p % m.ps;
+        if (col != at) {
+            at = col;
+            page = m.block_table[(int64_t)b * m.max_pages + col];
+        }
+        if (page >= 0 && page < m.num_pages) slot[j] = (int64_t)page * m.ps + (p - col * m.ps);
         else report(m.status, DSA_ERR_INVALID_ARG);
     }
     if (t + 4 <= m.max_tokens) {
@@ -111,15 +125,21 @@ __device__ __forceinline__ void write_maps(const Maps &m, int64_t t)
     }
 }
 
+// Every block of the cluster runs the same sums over the same lengths; the first one
+// writes the new ones, when all have read, and the pages are shared out among them.
 __global__ void __launch_bounds__(BL_THREADS)
 blocks_extend_kernel(const int32_t *new_lens, int32_t *context_lens, int32_t *pages_held, int32_t *block_table,
                      const int32_t *free_pages, int64_t free_capacity, int32_t *free_count, int32_t *token_start,
-                     Maps m, bool small)
+                     const Maps m, bool small)
 {
-    __shared__ int64_t sums[32];
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ Two sums[32];
     __shared__ int64_t ends[BL_THREADS];       // pages handed out up to and with each sequence of the chunk
     __shared__ int first_page[BL_THREADS];     // a sequence's pages before
-    const int tid = threadIdx.x;
+    __shared__ int32_t t_ends[BL_THREADS], lens[BL_THREADS];
+    const int tid = threadIdx.x, blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const bool writer = rank == 0;
+    grid_dep_wait();
     const int64_t count = free_count[0];
     const bool count_ok = count >= 0 && count <= free_capacity;
     if (!count_ok && tid == 0) report(m.status, DSA_ERR_INVALID_ARG);
@@ -141,64 +161,77 @@ blocks_extend_kernel(const int32_t *new_lens, int32_t *context_lens, int32_t *pa
                 }
             }
         }
-        int64_t total;
-        const int64_t upto = asked + block_scan(need, sums, &total);
-        asked += total;
+        // one pass of sums where no sequence is refused
+        Two total, upto = block_scan({need, grow}, sums, &total);
+        int64_t got = grow, pages = need;
         bool ok = grow > 0;
-        if (ok && need > 0 && (!count_ok || upto > count)) {
-            ok = false;
-            report(m.status, DSA_ERR_WORKSPACE);
-        }
-        const int64_t t_upto = offered + block_scan(ok ? grow : 0, sums, &total);
-        offered += total;
-        if (ok && t_upto > m.max_tokens) {
-            ok = false;
-            report(m.status, DSA_ERR_WORKSPACE);
-        }
-        const int64_t got = ok ? grow : 0, pages = ok ? need : 0;
-        const int64_t t_end = tokens + block_scan(got, sums, &total);
-        tokens += total;
-        const int64_t p_end = block_scan(pages, sums, &total);
-        ends[tid] = p_end;
-        first_page[tid] = (int)held;
-        if (b < m.B) {
-            token_start[b + 1] = (int32_t)t_end;
-            if (ok) {
-                context_lens[b] = (int32_t)(ctx + got);
-                pages_held[b] = (int32_t)(held + pages);
+        const bool tight = (need > 0 && (!count_ok || asked + upto.a > count)) || (ok && offered + upto.b > m.max_tokens);
+        if (__syncthreads_or(tight)) {
+            if (ok && need > 0 && (!count_ok || asked + upto.a > count)) {
+                ok = false;
+                report(m.status, DSA_ERR_WORKSPACE);
             }
+            asked += total.a;
+            const int64_t t_upto = offered + block_scan({ok ? grow : 0, 0}, sums, &total).a;
+            offered += total.a;
+            if (ok && t_upto > m.max_tokens) {
+                ok = false;
+                report(m.status, DSA_ERR_WORKSPACE);
+            }
+            got = ok ? grow : 0;
+            pages = ok ? need : 0;
+            upto = block_scan({pages, got}, sums, &total);
+        } else {
+            asked += total.a;
+            offered += total.b;
         }
-        if (b == 0) token_start[0] = 0;
-        __syncthreads();
+        const int64_t t_end = tokens + upto.b;
+        tokens += total.b;
+        ends[tid] = upto.a;
+        first_page[tid] = (int)held;
+        t_ends[tid] = (int32_t)t_end;
+        lens[tid] = (int32_t)(ctx + got);
+        cluster.sync();                // all have read the lengths; and the block its shared arrays
+        if (writer) {
+            if (b < m.B) {
+                token_start[b + 1] = (int32_t)t_end;
+                if (ok) {
+                    context_lens[b] = (int32_t)(ctx + got);
+                    pages_held[b] = (int32_t)(held + pages);
+                }
+            }
+            if (b == 0) token_start[0] = 0;
+        }
         // served sequences take their pages from the top of the stack in order: the
         // refused ones come behind the last that needs any, so the sums are dense
         const int64_t top = count - 1 - served;
-        for (int64_t i = tid; i < total; i += BL_THREADS) {
+        for (int64_t i = (int64_t)rank * BL_THREADS + tid; i < total.a; i += (int64_t)blocks * BL_THREADS) {
             const int s = upper(ends, BL_THREADS, i);
             const int64_t j = i - (s > 0 ? ends[s - 1] : 0);
             int32_t page = free_pages[top - i];
             if (page < 0 || page >= m.num_pages) page = -1;    // reported where its tokens are mapped
             block_table[(int64_t)(b0 + s) * m.max_pages + first_page[s] + j] = page;
         }
-        served += total;
-        __syncthreads();
+        served += total.a;
+        __syncthreads();               // the shared arrays may be written; this block's table is visible to it
     }
-    if (tid == 0 && count_ok) free_count[0] = (int32_t)(count - served);
+    if (writer && tid == 0 && count_ok && served > 0) free_count[0] = (int32_t)(count - served);
     if (small) {
-        __syncthreads();               // this block's global writes are visible to its threads
-        for (int64_t t = 4 * (int64_t)tid; t < m.max_tokens; t += 4 * BL_THREADS) write_maps(m, t);
+        const bool copied = m.B <= BL_THREADS;
+        for (int64_t t = 4 * (int64_t)tid; t < m.max_tokens; t += 4 * BL_THREADS)
+            write_maps(m, copied ? t_ends : m.token_start + 1, copied ? lens : m.context_lens, t);
     }
 }
 
 constexpr int BM_THREADS = 256;
 
 __global__ void __launch_bounds__(BM_THREADS)
-blocks_maps_kernel(Maps m)
+blocks_maps_kernel(const Maps m)
 {
     grid_dep_wait();                   // the tables and lengths of blocks_extend_kernel
     const int64_t step = 4 * (int64_t)gridDim.x * BM_THREADS;
     for (int64_t t = 4 * ((int64_t)blockIdx.x * BM_THREADS + threadIdx.x); t < m.max_tokens; t += step)
-        write_maps(m, t);
+        write_maps(m, m.token_start + 1, m.context_lens, t);
 }
 
 __global__ void __launch_bounds__(BL_THREADS)
@@ -206,15 +239,17 @@ blocks_trim_kernel(const int32_t *keep_lens, int32_t *context_lens, int32_t *pag
                    int32_t *free_pages, int64_t free_capacity, int32_t *free_count, int B, int max_pages,
                    int64_t num_pages, int ps, uint32_t *status)
 {
-    __shared__ int64_t sums[32];
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ Two sums[32];
     __shared__ int64_t ends[BL_THREADS];
     __shared__ int first_page[BL_THREADS];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const bool writer = rank == 0;
+    grid_dep_wait();
     const int64_t count = free_count[0];
     const bool count_ok = count >= 0 && count <= free_capacity;
     if (!count_ok && tid == 0) report(status, DSA_ERR_INVALID_ARG);
     const int64_t room = count_ok ? free_capacity - count : 0;
-    int64_t all = 0;                   // pages given back by all sequences
     // pages of one sequence to give back, 0 .. held; -1: the sequence is left alone
     auto freed_of = [&](int b, int &stay) -> int64_t {
         const int64_t ctx = context_lens[b], keep = keep_lens[b], held = pages_held[b];
@@ -223,42 +258,47 @@ blocks_trim_kernel(const int32_t *keep_lens, int32_t *context_lens, int32_t *pag
         return held - stay;
     };
     // first round: how many pages come back in all (the first of them goes on top)
-    int64_t asked = 0;
+    int64_t asked = 0, all = 0;
     for (int b0 = 0; b0 < B; b0 += BL_THREADS) {
         const int b = b0 + tid;
         int stay = 0;
-        int64_t freed = b < B ? max((int64_t)0, freed_of(b, stay)) : 0;
-        int64_t total;
-        const int64_t upto = asked + block_scan(freed, sums, &total);
-        asked += total;
-        if (upto > room) freed = 0;
-        block_scan(freed, sums, &total);
-        all += total;
+        const int64_t freed = b < B ? max((int64_t)0, freed_of(b, stay)) : 0;
+        Two total;
+        const int64_t upto = asked + block_scan({freed, 0}, sums, &total).a;
+        asked += total.a;
+        if (asked > room) block_scan({upto > room ? 0 : freed, 0}, sums, &total);
+        all += total.a;
     }
+    cluster.sync();                    // all have read free_count
     asked = 0;
     int64_t before = 0;
     for (int b0 = 0; b0 < B; b0 += BL_THREADS) {
         const int b = b0 + tid;
         int stay = 0;
-        int64_t freed = -1, total;
+        int64_t freed = -1;
         if (b < B) {
             freed = freed_of(b, stay);
             if (freed < 0) report(status, DSA_ERR_INVALID_ARG);
         }
-        const int64_t upto = asked + block_scan(max((int64_t)0, freed), sums, &total);
-        asked += total;
-        if (freed > 0 && upto > room) {
-            freed = -1;
-            report(status, DSA_ERR_WORKSPACE);
+        Two total;
+        int64_t end = block_scan({max((int64_t)0, freed), 0}, sums, &total).a;
+        const int64_t upto = asked + end;
+        asked += total.a;
+        if (asked > room) {
+            if (freed > 0 && upto > room) {
+                freed = -1;
+                report(status, DSA_ERR_WORKSPACE);
+            }
+            end = block_scan({max((int64_t)0, freed), 0}, sums, &total).a;
         }
-        ends[tid] = block_scan(max((int64_t)0, freed), sums, &total);
+        ends[tid] = end;
         first_page[tid] = stay;
-        if (freed >= 0) {
+        cluster.sync();                // all have read this chunk's lengths; and the block its shared arrays
+        if (writer && freed >= 0) {
             context_lens[b] = keep_lens[b];
             pages_held[b] = stay;
         }
-        __syncthreads();
-        for (int64_t i = tid; i < total; i += BL_THREADS) {
+        for (int64_t i = (int64_t)rank * BL_THREADS + tid; i < total.a; i += (int64_t)blocks * BL_THREADS) {
             const int s = upper(ends, BL_THREADS, i);
             const int64_t j = i - (s > 0 ? ends[s - 1] : 0);
             int32_t *entry = block_table + (int64_t)(b0 + s) * max_pages + first_page[s] + j;
@@ -270,10 +310,10 @@ blocks_trim_kernel(const int32_t *keep_lens, int32_t *context_lens, int32_t *pag
             *entry = -1;
             free_pages[count + all - 1 - before - i] = page;
         }
-        before += total;
+        before += total.a;
         __syncthreads();
     }
-    if (tid == 0 && count_ok) free_count[0] = (int32_t)(count + all);
+    if (writer && tid == 0 && count_ok && all > 0) free_count[0] = (int32_t)(count + all);
 }
 
 // ---------------------------------------------------------------- compaction
@@ -308,6 +348,7 @@ cache_compact_kernel(const CompactArgs a)
     const int b = blockIdx.x, tid = threadIdx.x;
     if (tid == 0) bad = 0;
     __syncthreads();
+    grid_dep_wait();
     const int64_t t0 = a.token_start[b], t1 = a.token_start[b + 1];
     const int64_t n = t1 - t0, ctx = a.context_lens[b], first = ctx - n;
     const int len = a.accept_len[b];
@@ -397,9 +438,8 @@ cudaError_t launch_blocks_extend(const int32_t *new_lens, int32_t *context_lens,
     Maps m{token_start, context_lens, block_table, B, max_pages, ps, num_pages, max_tokens,
            seq_ids, positions, slots, status};
     const bool small = max_tokens <= BL_SMALL;
-    blocks_extend_kernel<<<1, BL_THREADS, 0, st>>>(new_lens, context_lens, pages_held, block_table, free_pages,
-                                                   free_capacity, free_count, token_start, m, small);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_cluster(blocks_extend_kernel, 1, small ? 1 : BL_CLUSTER, BL_THREADS, st, new_lens, context_lens,
+                                   pages_held, block_table, free_pages, free_capacity, free_count, token_start, m, small);
     if (e != cudaSuccess || small) return e;
     const int64_t need = ceil_div(max_tokens, 4 * BM_THREADS);
     e = launch_chained(blocks_maps_kernel, dim3((unsigned)(need < 148 * 8 ? need : 148 * 8)), dim3(BM_THREADS), 0, st, m);
@@ -410,9 +450,9 @@ cudaError_t launch_blocks_trim(const int32_t *keep_lens, int32_t *context_lens, 
                                int32_t *block_table, int32_t *free_pages, int64_t free_capacity, int32_t *free_count,
                                int B, int max_pages, int64_t num_pages, int ps, uint32_t *status, cudaStream_t st)
 {
-    blocks_trim_kernel<<<1, BL_THREADS, 0, st>>>(keep_lens, context_lens, pages_held, block_table, free_pages,
-                                                 free_capacity, free_count, B, max_pages, num_pages, ps, status);
-    return cudaGetLastError();
+    const int blocks = (int64_t)B * max_pages <= BL_THREADS ? 1 : BL_CLUSTER;
+    return launch_cluster(blocks_trim_kernel, 1, blocks, BL_THREADS, st, keep_lens, context_lens, pages_held, block_table,
+                          free_pages, free_capacity, free_count, B, max_pages, num_pages, ps, status);
 }
 
 cudaError_t launch_cache_compact(const int32_t *block_table, const int32_t *context_lens, const int32_t *token_start,
@@ -426,8 +466,8 @@ cudaError_t launch_cache_compact(const int32_t *block_table, const int32_t *cont
                   {d_I, k_scale ? d : 2 * d, v_scale ? d : 2 * d},
                   {kscale_cache, k_scale, v_scale},
                   keep_lens, status};
-    cache_compact_kernel<<<(unsigned)B, CP_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    const cudaError_t e = launch_chained(cache_compact_kernel, dim3((unsigned)B), dim3(CP_THREADS), 0, st, a);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace dsa

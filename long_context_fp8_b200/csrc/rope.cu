@@ -111,6 +111,7 @@ rope_kernel(const __grid_constant__ RopeArgs a)
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
     const int rows = (int)min((int64_t)a.tokens, a.rows - row0);
     const int rot_units = INTERLEAVED ? a.half / 4 : a.half / 8;
+    grid_dep_wait();
     for (int i = threadIdx.x; i < rows * a.half; i += RP_THREADS) {
         const int r = i / a.half, p = i - r * a.half;
         const uint64_t phase = (uint64_t)(int64_t)a.positions[row0 + r] * a.turns[p];
@@ -188,14 +189,10 @@ rope_kernel(const __grid_constant__ RopeArgs a)
 template <typename T>
 cudaError_t launch_rope_t(const RopeArgs &a, bool interleaved, bool copy, dim3 grid, size_t smem, cudaStream_t st)
 {
-    if (interleaved) {
-        if (copy) rope_kernel<T, true, true><<<grid, RP_THREADS, smem, st>>>(a);
-        else rope_kernel<T, true, false><<<grid, RP_THREADS, smem, st>>>(a);
-    } else {
-        if (copy) rope_kernel<T, false, true><<<grid, RP_THREADS, smem, st>>>(a);
-        else rope_kernel<T, false, false><<<grid, RP_THREADS, smem, st>>>(a);
-    }
-    return cudaGetLastError();
+    auto kernel = interleaved ? (copy ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
+                              : (copy ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+    const cudaError_t e = launch_chained(kernel, grid, dim3(RP_THREADS), smem, st, a);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace

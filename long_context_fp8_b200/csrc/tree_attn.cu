@@ -36,6 +36,7 @@
 //           than 2^8, which is exact up to rounding.
 // Every mbarrier wait is bounded (DSA_ERR_TIMEOUT on expiry).
 #include <algorithm>
+#include <atomic>
 #include <numeric>
 
 #include <cuda_fp8.h>
@@ -51,6 +52,8 @@ using namespace sm100;
 constexpr int TA_M = 128;              // rows of a tile
 constexpr int TA_BLK = 128;            // cache rows of a block
 constexpr int TA_MAX_CTAS = 160;       // CTAs a workspace has room for (148 SMs)
+constexpr int TA_SEGS = 4;             // segments in the ring
+constexpr int TA_P0 = 6;               // sixteens of a block's weights that P V starts with (of 8)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.f;   // log2 units
@@ -73,12 +76,13 @@ struct TreeArgs {
     int rows_tok;                      // rows of a tile that one token takes: min(group, 128)
     int tile_tok;                      // tokens of a tile (1 when group > 128)
     int head_tiles;                    // tiles of one token (1 when group <= 128)
+    int cost_pair, cost_one;           // of a block of cache rows for a pair of tiles and for a single one
     float scale_log2;
     uint16_t *out;
     float *lse;
     int4 *desc;                        // [CTAs] first item of each CTA: sequence, head, tile, bits (1: cut, 2: pair)
     uint32_t *err;                     // [CTAs] dsa_status
-    float *part;                       // [2 CTAs][256][d] O / l
+    float *part;                       // [2 CTAs][d / 4][256][4] O / l: slot, columns, row
     float *part_lse;                   // [2 CTAs][256] log2 sum
     WsHeader *hdr;
 };
@@ -100,13 +104,17 @@ template <bool KV8, int D> struct Smem {
     static constexpr int scale_off = code_off + codes * code_tile;       // KV8: [block % 4][K, V][128]
     static constexpr int mask_off = scale_off + (KV8 ? 4 * 2 * 128 * 4 : 0);
     static constexpr int parent_off = mask_off + DSA_MAX_TREE * 16;
-    static constexpr int bar_off = parent_off + DSA_MAX_TREE * 2;
-    static constexpr int n_bars = 2 + 2 * slots + 6 + 3 + 2 * codes;
+    static constexpr int seg_off = parent_off + DSA_MAX_TREE * 2;        // ring of segments
+    static constexpr int bar_off = seg_off + TA_SEGS * 48;
+    static constexpr int n_bars = 2 + 2 * slots + 8 + 3 + 2 * TA_SEGS + 2 * codes;
     static constexpr int ctl_off = bar_off + 8 * n_bars;
     static constexpr int total = ctl_off + 240;
 };
 static_assert(Smem<false, 128>::total <= 232448 && Smem<false, 64>::total <= 232448, "shared memory of a CTA");
 static_assert(Smem<true, 128>::total <= 232448 && Smem<true, 64>::total <= 232448, "shared memory of a CTA");
+
+// A number as a type: for code that must know it when it is compiled.
+template <int N> struct Int { static constexpr int value = N; };
 
 // Control words of a CTA.
 struct Ctl {
@@ -123,16 +131,19 @@ static_assert(sizeof(Ctl) <= 240, "control words");
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 255) continue;         // reading the timer takes longer than most waits
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
         if (*abort) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (t - t0 > kWaitLimitNs) {
             *abort = 1;
             return false;
         }
     }
+    return true;
 }
 
 // 2^x by the SFU (2 ulp; results below 2^-126 flush to zero, which a sum that holds a term near 1 does not notice).
@@ -141,6 +152,23 @@ __device__ __forceinline__ float ex2_sfu(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 values in registers times two others.
+__device__ __forceinline__ void f2_scale(uint32_t &a, uint32_t &b, float fa, float fb)
+{
+    float x, y;
+    f2_unpack(f2_mul(f2_pack(__uint_as_float(a), __uint_as_float(b)), f2_pack(fa, fb)), x, y);
+    a = __float_as_uint(x);
+    b = __float_as_uint(y);
+}
+
+// The largest of three (sm_100's three-operand form).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Sixteen E4M3 codes as eight bf16 pairs, exactly.
@@ -177,17 +205,20 @@ struct Seq {
         tok0 = (int)t0;
         tiles = a.head_tiles > 1 ? n * a.head_tiles : (n + a.tile_tok - 1) / a.tile_tok;
         nblk = (ctx + TA_BLK - 1) / TA_BLK;
-        return (int64_t)tiles * nblk;
+        return (int64_t)((tiles >> 1) * a.cost_pair + (tiles & 1) * a.cost_one) * nblk;
     }
 };
 
 // The CTA's part of one item: blocks [blk0, blk1) for row tile `tile` (and the next, if `pair`).
-struct Segment {
-    int b, hk, tile, blk0, blk1;
-    bool pair;
+struct alignas(16) Segment {
+    int b, hk, tile, blk0;             // b: sequence, -1: no more
+    int blk1, pair, n, ctx;            // n, ctx, tok0, nblk: the sequence's tokens, context, first token, blocks
+    int tok0, nblk, pad0, pad1;
 };
 
-// Walks the CTA's share [c0, c1) of the list of work.  Every role walks it for itself.
+// Walks the CTA's share [c0, c1) of the list of work.  One warp does, and leaves the
+// segments in a ring in shared memory for the others (the walk's code in every role would not fit the
+// instruction cache).
 struct Walker {
     const TreeArgs &a;
     int64_t c0, c1, item;              // item: work before the current item
@@ -209,8 +240,9 @@ struct Walker {
         const int64_t rel = c0 - item;
         hk = (int)(rel / per_head);
         item += hk * per_head;
-        rg = (int)min((rel - hk * per_head) / (2 * s.nblk), (int64_t)(s.tiles - 1) / 2);
-        item += (int64_t)rg * 2 * s.nblk;
+        const int64_t per_pair = (int64_t)a.cost_pair * s.nblk;
+        rg = (int)min((rel - hk * per_head) / per_pair, (int64_t)(s.tiles - 1) / 2);
+        item += rg * per_pair;
     }
     __device__ __forceinline__ bool next(Segment &g)
     {
@@ -223,13 +255,18 @@ struct Walker {
                 hk = rg = 0;
                 continue;
             }
-            const int w = 2 * rg + 1 < s.tiles ? 2 : 1;
+            const bool pair = 2 * rg + 1 < s.tiles;
+            const int w = pair ? a.cost_pair : a.cost_one;
             const int64_t cost = (int64_t)w * s.nblk;
             const int64_t lo = max(c0 - item, (int64_t)0), hi = min(c1 - item, cost);
             g.b = b;
+            g.n = s.n;
+            g.ctx = s.ctx;
+            g.tok0 = s.tok0;
+            g.nblk = s.nblk;
             g.hk = hk;
             g.tile = 2 * rg;
-            g.pair = w == 2;
+            g.pair = pair;
             g.blk0 = (int)((lo + w - 1) / w);
             g.blk1 = (int)((hi + w - 1) / w);
             item += cost;
@@ -273,12 +310,14 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::bar_off);
     uint64_t *qfull = bars, *qempty = bars + 1, *kvfull = bars + 2, *kvempty = kvfull + SLOTS;
-    uint64_t *sfull = kvempty + SLOTS, *pfull = sfull + 2, *pvdone = pfull + 2, *oempty = pvdone + 2;
-    uint64_t *mfull = oempty + 1, *mempty = mfull + 1, *cfull = mempty + 1, *cempty = cfull + CODES;
+    uint64_t *sfull = kvempty + SLOTS, *pfull = sfull + 2, *pvdone = pfull + 4, *oempty = pvdone + 2;
+    uint64_t *mfull = oempty + 1, *mempty = mfull + 1, *gfull = mempty + 1, *gempty = gfull + TA_SEGS;
+    uint64_t *cfull = gempty + TA_SEGS, *cempty = cfull + CODES;
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::ctl_off);
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask_off);
     int16_t *par = reinterpret_cast<int16_t *>(smem + S::parent_off);
     float *scales = reinterpret_cast<float *>(smem + S::scale_off);
+    Segment *segs = reinterpret_cast<Segment *>(smem + S::seg_off);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int threads = blockDim.x;
@@ -287,14 +326,25 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         tmem_alloc(&ctl->tmem, 512);
         tmem_relinquish();
     }
+    if (tid == 32) {
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
     if (tid == 0) {
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         for (int i = 0; i < SLOTS; ++i) { mbar_init(&kvfull[i], KV8 ? 4 : 1); mbar_init(&kvempty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&sfull[i], 1); mbar_init(&pfull[i], 4); mbar_init(&pvdone[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[2 * i], 4);
+            mbar_init(&pfull[2 * i + 1], 4);
+            mbar_init(&pvdone[i], 1);
+        }
         mbar_init(oempty, 8);
         mbar_init(mfull, 1);
         mbar_init(mempty, 8);
+        for (int i = 0; i < TA_SEGS; ++i) { mbar_init(&gfull[i], 1); mbar_init(&gempty[i], KV8 ? 15 : 11); }
         if (KV8)
             for (int i = 0; i < CODES; ++i) { mbar_init(&cfull[i], 1); mbar_init(&cempty[i], 4); }
         ctl->abort = 0;
@@ -304,6 +354,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         ctl->s_issued[0] = ctl->s_issued[1] = ctl->pv_issued[0] = ctl->pv_issued[1] = 0;
         fence_mbar_init();
     }
+
+    grid_dep_wait();                   // what came before on the stream
 
     // ---- the CTA's share of the work: a sum over the sequences, then a search
     int64_t all = 0, mine = 0;
@@ -326,7 +378,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     all = 0;
     for (int w = 0; w < threads / 32; ++w) all += ctl->sums[w];
     // at least two blocks a CTA: shorter shares cost more to merge than they save
-    const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, all / 2));
+    const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, all / (2 * a.cost_one)));
     const bool works = (int64_t)blockIdx.x < ctas && all > 0;
     const int64_t c0 = works ? all * blockIdx.x / ctas : 0, c1 = works ? all * (blockIdx.x + 1) / ctas : 0;
     if (blockIdx.x == 0 && any_bad) ctl->err = DSA_ERR_INVALID_ARG;
@@ -371,11 +423,22 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     const uint32_t tmem = ctl->tmem;
     const uint32_t tS = tmem, tO = tmem + 256;     // S_x (and P_x in its first 64 columns), O_x
 
+    // The next segment of the ring (whole warps); false: there is none, or a wait ran out.
+    uint32_t seg_i = 0;
+    auto next = [&](Segment &g) -> bool {
+        const uint32_t st = seg_i % TA_SEGS;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&gfull[st], (seg_i / TA_SEGS) & 1, &ctl->abort))) return false;
+        g = segs[st];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&gempty[st]);
+        ++seg_i;
+        return g.b >= 0;
+    };
+
     if (warp < 4 || warp >= 12) {
         regs_dec<KV8 ? TA8_REGS_LOW : TA_REGS_LOW>();
         if (warp == 0) {
             // ------------------------------------------------ Q, K and V by TMA
-            Walker w(a, ctl);
             Segment g;
             const int nbox = TA_BLK / a.box;
             const int halves = KV8 ? 1 : S::halves;
@@ -384,20 +447,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             uint32_t t = 0;                        // tiles issued
             int item = 0;
             bool was_single = false, ok = true;
-            if (lane == 0) {
-                tma_prefetch_desc(&qmap);
-                tma_prefetch_desc(&kmap);
-                tma_prefetch_desc(&vmap);
-                int4 d = make_int4(-1, 0, 0, 0);
-                Walker w0(a, ctl);
-                Segment f;
-                if (w0.next(f)) d = make_int4(f.b, f.hk, f.tile, (f.blk0 > 0 ? 1 : 0) | (f.pair ? 2 : 0));
-                a.desc[blockIdx.x] = d;
-            }
-            __syncwarp();
-            for (; ok && w.next(g); ++item) {
-                const Seq s = w.s;
-                int row = cache_row(a, g.b, s.ctx, g.blk0 * TA_BLK + box * a.box, ctl);
+            for (; ok && next(g); ++item) {
+                int row = cache_row(a, g.b, g.ctx, g.blk0 * TA_BLK + box * a.box, ctl);
                 if (lane == 0) {
                     ok = wait_or_abort(qempty, (item & 1) ^ 1, &ctl->abort);
                     // every item's end is waited for in turn (a parity tells two phases apart, not
@@ -415,7 +466,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                             const int head = a.head_tiles > 1 ? (tl % a.head_tiles) * TA_M : 0;
                             for (int h = 0; h < S::halves; ++h)
                                 tma_load_4d(smem + S::q_off + x * S::tile + h * S::half, &qmap, qfull, h * 64, head, g.hk,
-                                            s.tok0 + tok);
+                                            g.tok0 + tok);
                         }
                     }
                 }
@@ -423,7 +474,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 was_single = !g.pair;
                 for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
                     const int here = row;
-                    if (blk + 1 < g.blk1) row = cache_row(a, g.b, s.ctx, (blk + 1) * TA_BLK + box * a.box, ctl);
+                    if (blk + 1 < g.blk1) row = cache_row(a, g.b, g.ctx, (blk + 1) * TA_BLK + box * a.box, ctl);
                     for (int kv = 0; kv < 2 && ok; ++kv, ++t) {
                         const int st = KV8 ? t % CODES : t % SLOTS;
                         const uint32_t ph = KV8 ? t / CODES : t / SLOTS;
@@ -446,84 +497,130 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             }
         } else if (warp == 1) {
             // ------------------------------------------------ S_x = Q_x K^T
-            if (lane == 0) {
-                constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, TA_BLK, false);
-                Walker w(a, ctl);
-                Segment g;
-                uint32_t i = 0, cnt[2] = {0, 0};   // blocks; products of each set
-                int item = 0;
-                bool ok = true;
-                for (; ok && w.next(g); ++item) {
-                    ok = wait_or_abort(qfull, item & 1, &ctl->abort);
-                    for (int blk = g.blk0; ok && blk < g.blk1; ++blk, ++i) {
-                        const uint32_t t = 2 * i, st = t % SLOTS;
-                        ok = wait_or_abort(&kvfull[st], (t / SLOTS) & 1, &ctl->abort);
-                        const uint32_t ka = smem_u32(smem + S::kv_off + st * S::tile);
-                        const int x0 = g.pair ? 0 : (blk - g.blk0) & 1, x1 = g.pair ? 1 : x0;
-                        for (int x = x0; ok && x <= x1; ++x) {
-                            // P_x lies in S_x: the last P V of the set must have read it
-                            ok = wait_or_abort(&pvdone[x], (cnt[x] & 1) ^ 1, &ctl->abort);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t qa = smem_u32(smem + S::q_off + (g.pair ? x : 0) * S::tile);
+            // (the whole warp keeps step, so that addresses stay in uniform registers; one lane issues)
+            constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, TA_BLK, false);
+            const uint64_t qd0 = umma_desc_k_sw128(smem_u32(smem + S::q_off));
+            const uint64_t kd0 = umma_desc_k_sw128(smem_u32(smem + S::kv_off));
+            Segment g;
+            uint32_t st = 0, ph = 0, cnt[2] = {0, 0};  // slot and its phase; products of each set
+            int item = 0;
+            bool ok = true;
+            auto product = [&](auto xc, uint64_t qd, uint64_t kd) {
+                constexpr int x = decltype(xc)::value;
+                // P_x lies in S_x: the last P V of the set must have read it
+                ok = __all_sync(0xffffffffu, ok && wait_or_abort(&pvdone[x], (cnt[x] & 1) ^ 1, &ctl->abort));
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_sync()) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                umma_f16(tS + x * 128, umma_desc_k_sw128(qa + (kk >> 2) * S::half + (kk & 3) * 32),
-                                         umma_desc_k_sw128(ka + (kk >> 2) * S::half + (kk & 3) * 32), idesc,
-                                         kk > 0 ? 1u : 0u);
-                            umma_commit(&sfull[x]);
-                            ctl->s_issued[x] = (int)++cnt[x];
-                        }
-                        if (ok) umma_commit(&kvempty[st]);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        constexpr int h = S::half >> 4;
+                        umma_f16(tS + x * 128, qd + (kk >> 2) * h + (kk & 3) * 2, kd + (kk >> 2) * h + (kk & 3) * 2, idesc,
+                                 kk > 0 ? 1u : 0u);
                     }
-                    if (ok) umma_commit(qempty);
+                    umma_commit(&sfull[x]);
+                    ctl->s_issued[x] = (int)cnt[x] + 1;
                 }
+                __syncwarp();
+                ++cnt[x];
+            };
+            for (; ok && next(g); ++item) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(qfull, item & 1, &ctl->abort));
+                for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&kvfull[st], ph, &ctl->abort));
+                    const uint64_t kd = kd0 + (uint64_t)(st * (S::tile >> 4));
+                    if (g.pair) {
+                        product(Int<0>{}, qd0, kd);
+                        product(Int<1>{}, qd0 + (S::tile >> 4), kd);
+                    } else if (((blk - g.blk0) & 1) == 0) {
+                        product(Int<0>{}, qd0, kd);
+                    } else {
+                        product(Int<1>{}, qd0, kd);
+                    }
+                    if (ok && elect_sync()) umma_commit(&kvempty[st]);
+                    __syncwarp();
+                    st += 2;
+                    if (st >= SLOTS) { st -= SLOTS; ph ^= 1; }
+                }
+                if (ok && elect_sync()) umma_commit(qempty);
+                __syncwarp();
             }
         } else if (warp == 2) {
             // ------------------------------------------------ O_x += P_x V
-            if (lane == 0) {
-                constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, D, true);
-                Walker w(a, ctl);
-                Segment g;
-                uint32_t i = 0, cnt[2] = {0, 0};
-                int item = 0;
-                bool ok = true;
-                for (; ok && w.next(g); ++item) {
-                    // the item before has read its O
-                    ok = wait_or_abort(oempty, (item & 1) ^ 1, &ctl->abort);
-                    for (int blk = g.blk0; ok && blk < g.blk1; ++blk, ++i) {
-                        const uint32_t t = 2 * i + 1, st = t % SLOTS;
-                        ok = wait_or_abort(&kvfull[st], (t / SLOTS) & 1, &ctl->abort);
-                        const uint32_t va = smem_u32(smem + S::kv_off + st * S::tile);
-                        const int x0 = g.pair ? 0 : (blk - g.blk0) & 1, x1 = g.pair ? 1 : x0;
-                        const bool first = g.pair ? blk == g.blk0 : blk - g.blk0 < 2;
-                        for (int x = x0; ok && x <= x1; ++x) {
-                            ok = wait_or_abort(&pfull[x], cnt[x] & 1, &ctl->abort);
-                            if (!ok) break;
-                            tc_fence_after();
+            constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, D, true);
+            const uint64_t vd0 = umma_desc_mn_sw128(smem_u32(smem + S::kv_off), S::half, 1024);
+            Segment g;
+            uint32_t st = 1, ph = 0, cnt[2] = {0, 0};
+            int item = 0;
+            bool ok = true;
+            auto product = [&](auto xc, uint64_t vd, bool first) {
+                constexpr int x = decltype(xc)::value;
+                // most of the columns as soon as their weights are there
 #pragma unroll
-                            for (int kk = 0; kk < TA_BLK / 16; ++kk)
-                                umma_f16_ts(tO + x * 128, tS + x * 128 + kk * 8,
-                                            umma_desc_mn_sw128(va + kk * 2048, S::half, 1024), idesc,
-                                            (first && kk == 0) ? 0u : 1u);
+                for (int h = 0; h < 2; ++h) {
+                    ok = __all_sync(0xffffffffu, ok && wait_or_abort(&pfull[2 * x + h], cnt[x] & 1, &ctl->abort));
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (elect_sync()) {
+#pragma unroll
+                        for (int kk = h * TA_P0; kk < (h ? TA_BLK / 16 : TA_P0); ++kk)
+                            umma_f16_ts(tO + x * 128, tS + x * 128 + kk * 8, vd + kk * 128, idesc,
+                                        (first && kk == 0) ? 0u : 1u);
+                        if (h == 1) {
                             umma_commit(&pvdone[x]);
-                            ctl->pv_issued[x] = (int)++cnt[x];
+                            ctl->pv_issued[x] = (int)cnt[x] + 1;
                         }
-                        if (ok) umma_commit(&kvempty[st]);
                     }
+                    __syncwarp();
+                }
+                ++cnt[x];
+            };
+            for (; ok && next(g); ++item) {
+                // the item before has read its O
+                ok = __all_sync(0xffffffffu, wait_or_abort(oempty, (item & 1) ^ 1, &ctl->abort));
+                for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&kvfull[st], ph, &ctl->abort));
+                    const uint64_t vd = vd0 + (uint64_t)(st * (S::tile >> 4));
+                    const int nth = blk - g.blk0;
+                    if (g.pair) {
+                        product(Int<0>{}, vd, nth == 0);
+                        product(Int<1>{}, vd, nth == 0);
+                    } else if ((nth & 1) == 0) {
+                        product(Int<0>{}, vd, nth < 2);
+                    } else {
+                        product(Int<1>{}, vd, nth < 2);
+                    }
+                    if (ok && elect_sync()) umma_commit(&kvempty[st]);
+                    __syncwarp();
+                    st += 2;
+                    if (st >= SLOTS) { st -= SLOTS; ph ^= 1; }
                 }
             }
         } else if (warp == 3) {
-            // ------------------------------------------------ ancestors of each token
+            // ------------------------------------------------ segments, and each token's ancestors
             // Bit j of token i: j is i or above it.  0 for a padding row (and under one).
             Walker w(a, ctl);
             Segment g;
             int cur = -1, seq = 0;
             bool ok = true;
-            while (ok && w.next(g)) {
+            while (ok) {
+                const bool more = w.next(g);
+                const uint32_t st = seg_i % TA_SEGS;
+                ok = __all_sync(0xffffffffu, wait_or_abort(&gempty[st], ((seg_i / TA_SEGS) & 1) ^ 1, &ctl->abort));
+                if (!ok) break;
+                if (!more) g.b = -1;
+                if (lane == 0) {
+                    if (seg_i == 0)
+                        a.desc[blockIdx.x] = make_int4(g.b, g.hk, g.tile, (g.blk0 > 0 ? 1 : 0) | (g.pair ? 2 : 0));
+                    segs[st] = g;
+                    mbar_arrive(&gfull[st]);
+                }
+                __syncwarp();
+                ++seg_i;
+                if (!more) break;
                 if (g.b == cur) continue;
                 cur = g.b;
-                const Seq s = w.s;
+                const Segment &s = g;
                 int p[DSA_MAX_TREE / 32];
 #pragma unroll
                 for (int j = 0; j < DSA_MAX_TREE / 32; ++j) {
@@ -562,12 +659,11 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             // Every E4M3 value is a bf16 value.  Thread i brings the two scales of
             // row i of a block, a block ahead (their addresses go through the page table).
             const int ct = tid - 384;
-            Walker w(a, ctl);
             Segment g;
             uint32_t t = 0, i = 0;
             bool ok = true;
-            while (ok && w.next(g)) {
-                const Seq s = w.s;
+            while (ok && next(g)) {
+                const Segment &s = g;
                 const int64_t none = a.num_pages * a.page_size;
                 auto row_of = [&](int blk) -> int64_t {
                     return blk < g.blk1 ? cache_row(a, g.b, s.ctx, blk * TA_BLK + ct, ctl) : none;
@@ -626,7 +722,6 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         const uint32_t tSx = tS + x * 128 + trow, tOx = tO + x * 128 + trow;
         float *ml = reinterpret_cast<float *>(smem + S::ml_off);
         const int tr = r / a.rows_tok, hr = r - tr * a.rows_tok;
-        Walker w(a, ctl);
         Segment g;
         uint32_t cnt[2] = {0, 0}, i0 = 0;          // products of each set; blocks before this segment
         int cur = -1, seqs = 0;                    // sequence, and how many before it
@@ -645,12 +740,12 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             ++seqs;
             masked = false;
         };
-        while (w.next(g)) {
+        while (next(g)) {
             if (g.b != cur) {
                 leave();
                 cur = g.b;
             }
-            const Seq s = w.s;
+            const Segment &s = g;
             const int prefix = s.ctx - s.n;
             const int tile = g.tile + (g.pair ? x : 0);
             const int tok = (a.head_tiles > 1 ? tile / a.head_tiles : tile * a.tile_tok) + tr;
@@ -677,10 +772,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                     for (int c = 0; c < 32; ++c) {
                         const float4 f = sc[c];
                         uint32_t *u = &v[c >> 3][(c & 7) * 4];
-                        u[0] = __float_as_uint(__uint_as_float(u[0]) * f.x);
-                        u[1] = __float_as_uint(__uint_as_float(u[1]) * f.y);
-                        u[2] = __float_as_uint(__uint_as_float(u[2]) * f.z);
-                        u[3] = __float_as_uint(__uint_as_float(u[3]) * f.w);
+                        f2_scale(u[0], u[1], f.x, f.y);
+                        f2_scale(u[2], u[3], f.z, f.w);
                     }
                 }
                 if ((blk + 1) * TA_BLK > prefix) {
@@ -713,56 +806,64 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                         fence_proxy_async_smem();
                     }
                 }
-                float mx[8];
+                float mx[4];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) mx[q] = __uint_as_float(v[0][q]);
+                for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(v[q][0]);
 #pragma unroll
-                for (int q = 8; q < 128; ++q) mx[q & 7] = fmaxf(mx[q & 7], __uint_as_float(v[q >> 5][q & 31]));
-                const float mr = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                for (int q = 1; q < 31; q += 2)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(v[c][q]), __uint_as_float(v[c][q + 1]));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][31]));
+                const float mr = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 const float mb = mr * a.scale_log2;            // the scale is positive
-                float m_new = m, alpha = 1.f;
-                if (mb > m + kRescaleThreshold || (m == -INFINITY && mb != -INFINITY)) {
-                    m_new = mb;
-                    alpha = m == -INFINITY ? 0.f : exp2f(m - m_new);
-                }
-                const float base = m_new == -INFINITY ? 0.f : m_new;
-                const bool need = blk > b_first && alpha != 1.f;
+                const bool grows = mb > m + kRescaleThreshold || (m == -INFINITY && mb != -INFINITY);
                 // tcgen05.ld/st take the whole warp; the last P V of this set is done (S waited for it)
-                if (__any_sync(0xffffffffu, need)) {
-                    const float f = need ? alpha : 1.f;
+                if (__any_sync(0xffffffffu, grows)) {
+                    const float f = grows ? (m == -INFINITY ? 0.f : exp2f(m - mb)) : 1.f;
+                    if (blk > b_first) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(tOx + c * 32, o);
+                            tmem_wait_ld_dep32(o);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tOx + c * 32, o);
-                        tmem_wait_ld_dep32(o);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-                        tmem_st32(tOx + c * 32, o);
+                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                            tmem_st32(tOx + c * 32, o);
+                        }
                     }
+                    l *= f;
+                    if (grows) m = mb;
                 }
+                const float base = m == -INFINITY ? 0.f : m;
                 const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nb2 = f2_pack(-base, -base);
                 const uint64_t one2 = f2_pack(1.f, 1.f);
                 uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
                 const float4 *vs4 = reinterpret_cast<const float4 *>(scales + (i & 3) * 256 + 128);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {                  // 64 columns: 32 words of P
-                    uint32_t pk[32];
+                for (int c = 0; c < 4; ++c) {                  // 32 columns: 16 words of P
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        const uint32_t *u = &v[2 * c + (q >> 4)][(2 * q) & 31];
+                    for (int q = 0; q < 16; ++q) {
+                        const uint32_t *u = &v[c][2 * q];
                         float x0, x1;
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), sc2, nb2), x0, x1);
                         float p0 = ex2_sfu(x0), p1 = ex2_sfu(x1);
                         rs2[q & 3] = f2_fma(f2_pack(p0, p1), one2, rs2[q & 3]);
                         if (KV8) {
-                            const float4 f = vs4[c * 16 + (q >> 1)];
-                            p0 *= (q & 1) ? f.z : f.x;
-                            p1 *= (q & 1) ? f.w : f.y;
+                            const float4 f = vs4[c * 8 + (q >> 1)];
+                            f2_unpack(f2_mul(f2_pack(p0, p1), (q & 1) ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y)), p0, p1);
                         }
                         pk[q] = pack_bf16x2(p0, p1);           // the products' precision: one rounding of each weight
                     }
-                    tmem_st32(tSx + c * 32, pk);
+                    tmem_st16(tSx + c * 16, pk);
+                    if (c >= 2) {
+                        static_assert(TA_P0 == 6, "three of four stores come before P V starts");
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pfull[2 * x + c - 2]);
+                    }
                 }
                 float rsum = 0.f;
 #pragma unroll
@@ -771,12 +872,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                     f2_unpack(rs2[q], lo, hi);
                     rsum += lo + hi;
                 }
-                l = l * alpha + rsum;
-                m = m_new;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[x]);
+                l += rsum;
             }
             // ---- the item's end (or this CTA's part of it)
             const int n0 = g.pair ? nb : (nb + 1) / 2, n1 = g.pair ? nb : nb / 2;
@@ -811,7 +907,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             const float g_own = f_own * inv, g_oth = f_oth * inv;
             const bool whole = g.blk0 == 0 && g.blk1 == s.nblk;
             // slot 0: an item that began in an earlier CTA, 1: one that ends in a later CTA
-            const int64_t prow = ((int64_t)blockIdx.x * 2 + (g.blk0 > 0 ? 0 : 1)) * 256 + (g.pair ? x * 128 : 0) + r;
+            const int64_t pslot = (int64_t)blockIdx.x * 2 + (g.blk0 > 0 ? 0 : 1);
+            const int prow = (g.pair ? x * 128 : 0) + r;
             const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + g.hk * a.group + head;
             // a single tile: set x takes half of the columns of both parts
             const int col0 = g.pair ? 0 : x * (D / 2), cols = g.pair ? D : D / 2;
@@ -847,14 +944,16 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                                               pack_bf16x2(acc[8 * u + 4], acc[8 * u + 5]), pack_bf16x2(acc[8 * u + 6], acc[8 * u + 7]));
                     }
                 } else if (valid) {
-                    float4 *p = reinterpret_cast<float4 *>(a.part + prow * D + c);
+                    // four columns of all 256 rows lie side by side: a warp stores 512 bytes at a time
+                    float4 *p = reinterpret_cast<float4 *>(a.part) + pslot * (D / 4 * 256) + (c / 4) * 256 + prow;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) p[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
+                    for (int u = 0; u < 8; ++u)
+                        p[u * 256] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
                 }
             }
             if (valid && (g.pair || x == 0)) {
                 const float l2 = lives && lt > 0.f ? mt + log2f(lt) : -INFINITY;
-                if (!whole) a.part_lse[prow] = l2;
+                if (!whole) a.part_lse[pslot * 256 + prow] = l2;
                 else if (a.lse) a.lse[orow] = lives && lt > 0.f ? mt * kLn2 + logf(lt) : -INFINITY;
             }
             tc_fence_before();
@@ -908,7 +1007,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 // Parts of a cut item: the last of the CTA where it began (slot 1), and the first
 // (slot 0) of every CTA behind it up to its end.
 //   out = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M),  L_i the parts' log2 sums.
-constexpr int TM_THREADS = 256;
+constexpr int TM_THREADS = 256;        // rows of two tiles
+constexpr int TM_QUADS = 4;            // sixteen columns: 32 bytes of output, a sector
 
 template <int D>
 __global__ void __launch_bounds__(TM_THREADS)
@@ -945,10 +1045,10 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
         }
     }
     __syncthreads();
-    // a warp per row: 256 rows an item
-    for (int64_t u = (int64_t)blockIdx.x * (TM_THREADS / 32) + warp; u < (int64_t)n_items * 256;
-         u += (int64_t)gridDim.x * (TM_THREADS / 32)) {
-        const int c = first[u >> 8], row = (int)(u & 255);
+    // a block per item and TM_QUADS column quads, a thread per row
+    constexpr int groups = D / 4 / TM_QUADS;
+    for (int u = blockIdx.x; u < n_items * groups; u += gridDim.x) {
+        const int c = first[u / groups], quad = (u % groups) * TM_QUADS, row = tid;
         const int4 d = desc[c];
         Seq s;
         bool bad;
@@ -962,44 +1062,59 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
         int parts = 1;
         while (c + parts - 1 < ctas && (desc[c + parts - 1].w & 1) && same(c, c + parts - 1)) ++parts;
         // part 0: slot 1 of CTA c - 1; part p: slot 0 of CTA c - 1 + p
-        auto at = [&](int p) -> int64_t { return ((int64_t)(c - 1 + p) * 2 + (p == 0 ? 1 : 0)) * 256 + row; };
-        float M = -INFINITY;
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, a.part_lse[at(p)]);
+        auto at = [&](int p) -> int64_t { return (int64_t)(c - 1 + p) * 2 + (p == 0 ? 1 : 0); };
+        const float4 *part = reinterpret_cast<const float4 *>(a.part) + quad * 256 + row;
+        // one pass: sums relative to the largest part so far
+        float M = -INFINITY, sum = 0.f;
+        float4 acc[TM_QUADS];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        constexpr int E = D / 32;
-        float acc[E], sum = 0.f;
+        for (int e = 0; e < TM_QUADS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = 0; p0 < parts; p0 += 4) {
+            float L[4];
+            float4 o[4][TM_QUADS];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        if (M != -INFINITY) {
-            for (int p0 = 0; p0 < parts; p0 += 8) {
-                float wt[8], o[8][E];
+            for (int q = 0; q < 4; ++q) {
+                L[q] = -INFINITY;
+                if (p0 + q >= parts) continue;
+                L[q] = a.part_lse[at(p0 + q) * 256 + row];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    wt[q] = 0.f;
-                    if (p0 + q >= parts) continue;
-                    wt[q] = exp2f(a.part_lse[at(p0 + q)] - M);
-                    const float *po = a.part + at(p0 + q) * D + lane * E;
-                    if (E == 4) *reinterpret_cast<float4 *>(o[q]) = *reinterpret_cast<const float4 *>(po);
-                    else *reinterpret_cast<float2 *>(o[q]) = *reinterpret_cast<const float2 *>(po);
-                }
+                for (int e = 0; e < TM_QUADS; ++e) o[q][e] = part[at(p0 + q) * (D / 4 * 256) + e * 256];
+            }
+            const float top = fmaxf(fmaxf(fmaxf(L[0], L[1]), fmaxf(L[2], L[3])), M);
+            if (top == -INFINITY) continue;
+            const float f = exp2f(M - top);
+            M = top;
+            sum *= f;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    if (p0 + q >= parts) continue;
-                    sum += wt[q];
+            for (int e = 0; e < TM_QUADS; ++e) {
+                acc[e].x *= f;
+                acc[e].y *= f;
+                acc[e].z *= f;
+                acc[e].w *= f;
+            }
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += wt[q] * o[q][e];
+            for (int q = 0; q < 4; ++q) {
+                if (p0 + q >= parts) continue;
+                const float wt = exp2f(L[q] - M);
+                sum += wt;
+#pragma unroll
+                for (int e = 0; e < TM_QUADS; ++e) {
+                    acc[e].x += wt * o[q][e].x;
+                    acc[e].y += wt * o[q][e].y;
+                    acc[e].z += wt * o[q][e].z;
+                    acc[e].w += wt * o[q][e].w;
                 }
             }
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + d.y * a.group + head;
-        uint32_t w2[E / 2];
+        uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * D + quad * 4);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) w2[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        if (E == 4) *reinterpret_cast<uint2 *>(a.out + orow * D + lane * E) = make_uint2(w2[0], w2[E / 2 - 1]);
-        else *reinterpret_cast<uint32_t *>(a.out + orow * D + lane * E) = w2[0];
-        if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? M * kLn2 + logf(sum) : -INFINITY;
+        for (int e = 0; e < TM_QUADS; e += 2)
+            out[e / 2] = make_uint4(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv),
+                                    pack_bf16x2(acc[e + 1].x * inv, acc[e + 1].y * inv),
+                                    pack_bf16x2(acc[e + 1].z * inv, acc[e + 1].w * inv));
+        if (quad == 0 && a.lse) a.lse[orow] = sum > 0.f ? M * kLn2 + logf(sum) : -INFINITY;
     }
 }
 
@@ -1009,17 +1124,26 @@ cudaError_t launch_tree_t(const CUtensorMap &qmap, const CUtensorMap &kmap, cons
 {
     auto kernel = KV8 ? tree_attn_kv8_kernel<D> : tree_attn_kernel<D>;
     constexpr int smem = Smem<KV8, D>::total;
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    // once a device
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // the register split assumes it: an error, not a wait that never ends
-    if (fa.numRegs != (KV8 ? TA8_REGS : TA_REGS)) return cudaErrorInvalidKernelImage;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        // the register split assumes it: an error, not a wait that never ends
+        if (fa.numRegs != (KV8 ? TA8_REGS : TA_REGS)) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    e = launch_chained(kernel, dim3((unsigned)ctas), dim3(KV8 ? TA8_THREADS : TA_THREADS), smem, st, qmap, kmap, vmap, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, KV8 ? TA8_THREADS : TA_THREADS, smem, st>>>(qmap, kmap, vmap, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = launch_chained(tree_merge_kernel<D>, dim3(148 * 4), dim3(TM_THREADS), 0, st, a, ctas);
+    e = launch_chained(tree_merge_kernel<D>, dim3((unsigned)std::max(1, (ctas - 1) * (D / 4 / TM_QUADS))), dim3(TM_THREADS), 0, st, a, ctas);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -1070,6 +1194,8 @@ cudaError_t launch_tree_attn(const uint16_t *q, const void *k, const float *ks, 
     a.rows_tok = std::min(a.group, TA_M);
     a.tile_tok = TA_M / a.rows_tok;
     a.head_tiles = (int)ceil_div(a.group, TA_M);
+    a.cost_pair = ks ? 1 : 2;
+    a.cost_one = 1;
     a.scale_log2 = sm_scale * kLog2e;
     a.out = out;
     a.lse = lse;

@@ -94,6 +94,7 @@ verify_tree_kernel(const VerifyArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / blocks;
+    grid_dep_wait();
     const int64_t t0 = a.token_start[b], t1 = a.token_start[b + 1];
     const int64_t n64 = t1 - t0;
     const bool sane = t0 >= 0 && n64 >= 0 && t1 <= a.N && n64 <= DSA_MAX_TREE;
@@ -300,18 +301,7 @@ cudaError_t launch_verify_tree(const float *target, const float *draft, const in
     // 512 threads an SM), so that a row is read by as many SMs as there are
     int blocks = 8;
     while (blocks > 1 && (int64_t)B * blocks > 148 * 4) blocks /= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)B * blocks);
-    cfg.blockDim = dim3(VF_THREADS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = blocks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_tree_kernel, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_cluster(verify_tree_kernel, (unsigned)B, (unsigned)blocks, VF_THREADS, st, a);
 }
 
 }  // namespace dsa

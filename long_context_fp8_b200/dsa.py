@@ -8,7 +8,6 @@ an error status, a ``DSAError`` is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -613,36 +612,21 @@ ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
 MAX_TREE = 128
 
 
-def _on(ref: torch.Tensor):
-    """Device context of a call: the tensors' device, where it is not the current one."""
-    if ref.device.index in (None, torch.cuda.current_device()):
-        return contextlib.nullcontext()
-    return torch.cuda.device(ref.device)
+_bound = None
 
 
-def _t(t: Optional[torch.Tensor], dtype, ref: torch.Tensor, shape=None):
-    """Address of a contiguous tensor of that type (and shape) on ref's device."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise ValueError(f"expected {dtype}, got {t.dtype}")
-    if t.device != ref.device:
-        raise ValueError(f"tensors on {t.device} and {ref.device}")
-    if not t.is_contiguous():
-        raise ValueError("DSA entry points take contiguous tensors")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _cuda(t: torch.Tensor) -> torch.Tensor:
-    if not t.is_cuda:
-        raise ValueError("DSA entry points take CUDA tensors")
-    return t
-
-
-def _raw_stream(stream, ref: torch.Tensor) -> int:
-    return torch.cuda.current_stream(ref.device).cuda_stream if stream is None else stream.cuda_stream
+def _binding():
+    """The compiled binding (its checks raise ValueError, a status DSAError)."""
+    global _bound
+    if _bound is None:
+        load()
+        try:
+            from . import _bind
+        except ImportError as e:
+            raise RuntimeError("DSA binding not found; build it with `python -m long_context_fp8_b200.build`") from e
+        _bind.init(LIB_PATH, DSAError)
+        _bound = _bind
+    return _bound
 
 
 def dsa_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -655,16 +639,6 @@ def dsa_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", f
     return turns
 
 
-def _rope_rows(x: torch.Tensor, like: Optional[torch.Tensor] = None) -> int:
-    """Address check of [rows, H, d] with dense heads and any row stride."""
-    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1) or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
-        raise ValueError("dsa_rope takes [rows, H, d] with dense heads")
-    if like is not None and (x.shape != like.shape or x.dtype != like.dtype or x.device != like.device):
-        raise ValueError("dsa_rope's tensors must agree in shape, type and device")
-    # a single row's stride says nothing
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
-
-
 def dsa_rope(q, positions, freqs, k=None, rot_begin=0, interleaved=False, attn_factor=1.0, inverse=False,
              q_out=None, k_out=None, stream=None):
     """Rotary positions of q [rows, H_q, d] and k [rows, H_k, d] (bf16 or fp32,
@@ -672,29 +646,8 @@ def dsa_rope(q, positions, freqs, k=None, rot_begin=0, interleaved=False, attn_f
     ``rot_begin`` on, by ``positions`` int32 [rows] and dsa_rope_freqs' table.
     ``inverse``: the gradient of the forward call.  ``q_out is q`` rotates in
     place.  Returns (q_out, k_out)."""
-    rows, H_q, d = _cuda(q).shape
-    dt = _val_dtype(q)
-    qs = _rope_rows(q)
-    if q_out is None:
-        q_out = torch.empty((rows, H_q, d), dtype=q.dtype, device=q.device)
-    qos = _rope_rows(q_out, q)
-    kp = kop = None
-    ks = kos = H_k = 0
-    if k is not None:
-        H_k = k.shape[1]
-        if k.shape[0] != rows or k.shape[2] != d or k.dtype != q.dtype or k.device != q.device:
-            raise ValueError("q and k must agree in rows, head dimension, type and device")
-        ks = _rope_rows(k)
-        if k_out is None:
-            k_out = torch.empty((rows, H_k, d), dtype=k.dtype, device=k.device)
-        kos = _rope_rows(k_out, k)
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    with _on(q):
-        st = load().dsa_rope(q.data_ptr(), qs, H_q, kp, ks, H_k, _t(positions, torch.int32, q, (rows,)), rows, d,
-                             rot_begin, 2 * len(freqs), int(bool(interleaved)), ctypes.addressof(freqs), attn_factor,
-                             int(bool(inverse)), q_out.data_ptr(), qos, kop, kos, dt, _raw_stream(stream, q))
-    _check("dsa_rope", st)
-    return q_out, k_out
+    return (_bound or _binding()).rope(q, k, positions, ctypes.addressof(freqs), 2 * len(freqs), rot_begin, interleaved,
+                                       attn_factor, inverse, q_out, k_out, stream)
 
 
 def dsa_blocks_extend(pool: dict, new_lens, page_size: int, num_pages: int, max_tokens: int, plan=None, status=None,
@@ -705,23 +658,16 @@ def dsa_blocks_extend(pool: dict, new_lens, page_size: int, num_pages: int, max_
     free_count [1].  Returns ``plan``: token_start [B + 1], seq_ids and
     positions [max_tokens], slots int64 [max_tokens] (-1 behind the last
     token).  ``status``: as in dsa_cache_append."""
-    bt = _cuda(pool["block_table"])
-    B, max_pages = bt.shape
-    i32, dev = torch.int32, bt.device
+    bt = pool["block_table"]
     if plan is None:
-        plan = {"token_start": torch.empty(B + 1, dtype=i32, device=dev),
-                "seq_ids": torch.empty(max_tokens, dtype=i32, device=dev),
-                "positions": torch.empty(max_tokens, dtype=i32, device=dev),
-                "slots": torch.empty(max_tokens, dtype=torch.int64, device=dev)}
-    free = pool["free_pages"]
-    with _on(bt):
-        st = load().dsa_blocks_extend(
-            _t(new_lens, i32, bt, (B,)), _t(pool["context_lens"], i32, bt, (B,)), _t(pool["pages_held"], i32, bt, (B,)),
-            _t(bt, i32, bt), _t(free, i32, bt), free.numel(), _t(pool["free_count"], i32, bt, (1,)), B, max_pages,
-            num_pages, page_size, max_tokens, _t(plan["token_start"], i32, bt, (B + 1,)),
-            _t(plan["seq_ids"], i32, bt, (max_tokens,)), _t(plan["positions"], i32, bt, (max_tokens,)),
-            _t(plan.get("slots"), torch.int64, bt, (max_tokens,)), _t(status, i32, bt), _raw_stream(stream, bt))
-    _check("dsa_blocks_extend", st)
+        i32 = dict(dtype=torch.int32, device=bt.device)
+        plan = {"token_start": torch.empty(bt.shape[0] + 1, **i32), "seq_ids": torch.empty(max_tokens, **i32),
+                "positions": torch.empty(max_tokens, **i32),
+                "slots": torch.empty(max_tokens, dtype=torch.int64, device=bt.device)}
+    (_bound or _binding()).blocks_extend(bt, pool["context_lens"], pool["pages_held"], pool["free_pages"],
+                                         pool["free_count"], new_lens, page_size, num_pages, max_tokens,
+                                         plan["token_start"], plan["seq_ids"], plan["positions"], plan.get("slots"),
+                                         status, stream)
     return plan
 
 
@@ -729,17 +675,11 @@ def dsa_blocks_trim(pool: dict, keep_lens, page_size: int, num_pages: Optional[i
     """Cut every sequence back to keep_lens[b] tokens and give the pages behind
     them back to the pool (as in dsa_blocks_extend).  ``num_pages`` bounds the
     page ids (default: the largest that page_size allows)."""
-    bt = _cuda(pool["block_table"])
-    B, max_pages = bt.shape
-    i32 = torch.int32
-    free = pool["free_pages"]
-    num_pages = (2 ** 31 - 1) // page_size if num_pages is None and page_size > 0 else num_pages
-    with _on(bt):
-        st = load().dsa_blocks_trim(
-            _t(keep_lens, i32, bt, (B,)), _t(pool["context_lens"], i32, bt, (B,)), _t(pool["pages_held"], i32, bt, (B,)),
-            _t(bt, i32, bt), _t(free, i32, bt), free.numel(), _t(pool["free_count"], i32, bt, (1,)), B, max_pages,
-            num_pages, page_size, _t(status, i32, bt), _raw_stream(stream, bt))
-    _check("dsa_blocks_trim", st)
+    if num_pages is None:
+        num_pages = (2 ** 31 - 1) // max(page_size, 1)
+    (_bound or _binding()).blocks_trim(pool["block_table"], pool["context_lens"], pool["pages_held"],
+                                       pool["free_pages"], pool["free_count"], keep_lens, page_size, num_pages, status,
+                                       stream)
 
 
 def tree_attn_workspace_size(B, N, H_q, H_kv, d) -> int:
@@ -753,33 +693,11 @@ def dsa_tree_attn(inp: dict, max_tree: int, max_context: int, sm_scale=None, out
     k_cache_scale, v_cache_scale [P, page_size(, H_kv)]; block_table,
     context_lens (drafts included), token_start [B + 1] and parents [N]
     int32.  A caller that keeps the workspace (``ws``) saves its allocation."""
-    q, kc, bt = _cuda(inp["q"]), inp["k_cache"], inp["block_table"]
-    N, H_q, d = q.shape
-    P, ps = kc.shape[0], kc.shape[1]
-    H_kv = kc.shape[2] if kc.dim() == 4 else 1
-    B, max_pages = bt.shape
-    i32, f32 = torch.int32, torch.float32
-    sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
-    lib = load()
-    if ws is None:
-        ws = workspace(lib.dsa_tree_attn_workspace_size(B, N, H_q, H_kv, d), q.device)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((N, H_q), dtype=f32, device=q.device)
-    ksc, vsc = inp.get("k_cache_scale"), inp.get("v_cache_scale")
-    if kc.shape[-1] != d:
-        raise ValueError(f"expected cache rows of {d} values, got {kc.shape[-1]}")
-    code, scale_shape = torch.bfloat16 if ksc is None else torch.uint8, kc.shape[:-1]
-    with _on(q):
-        st = lib.dsa_tree_attn(_t(q, torch.bfloat16, q), _t(kc, code, q), _t(ksc, f32, q, scale_shape),
-                               _t(inp["v_cache"], code, q, kc.shape), _t(vsc, f32, q, scale_shape), _t(bt, i32, q),
-                               _t(inp["context_lens"], i32, q, (B,)), _t(inp["token_start"], i32, q, (B + 1,)),
-                               _t(inp["parents"], i32, q, (N,)), P, max_pages, ps, B, N, max_tree, max_context, H_q,
-                               H_kv, d, sm_scale, _t(out, torch.bfloat16, q, q.shape), _t(lse, f32, q, (N, H_q)),
-                               _t(ws, torch.uint8, q), ws.numel(), _raw_stream(stream, q))
-    _check("dsa_tree_attn", st)
-    return out, lse
+    get = inp.get
+    return (_bound or _binding()).tree_attn(inp["q"], inp["k_cache"], get("k_cache_scale"), inp["v_cache"],
+                                            get("v_cache_scale"), inp["block_table"], inp["context_lens"],
+                                            inp["token_start"], inp["parents"], max_tree, max_context, sm_scale, out, lse,
+                                            ws, stream)
 
 
 def dsa_verify_tree(target_probs, draft_probs, tokens, parents, token_start, u_accept, u_sample, max_path=None,
@@ -789,25 +707,8 @@ def dsa_verify_tree(target_probs, draft_probs, tokens, parents, token_start, u_a
     u_accept f32 [N], u_sample f32 [B] -> (path int32 [B, max_path],
     accept_len int32 [B], next_token int32 [B]).  ``status``: as in
     dsa_cache_append."""
-    N, V = _cuda(target_probs).shape
-    B = u_sample.shape[0]
-    i32, f32, ref = torch.int32, torch.float32, target_probs
-    if path is None:
-        path = torch.empty((B, MAX_TREE if max_path is None else max_path), dtype=i32, device=ref.device)
-    elif max_path not in (None, path.shape[1]):
-        raise ValueError("path's width is max_path")
-    if accept_len is None:
-        accept_len = torch.empty((B,), dtype=i32, device=ref.device)
-    if next_token is None:
-        next_token = torch.empty((B,), dtype=i32, device=ref.device)
-    with _on(ref):
-        st = load().dsa_verify_tree(_t(ref, f32, ref), _t(draft_probs, f32, ref, ref.shape), _t(tokens, i32, ref, (N,)),
-                                    _t(parents, i32, ref, (N,)), _t(token_start, i32, ref, (B + 1,)),
-                                    _t(u_accept, f32, ref, (N,)), _t(u_sample, f32, ref, (B,)), B, N, V, path.shape[1],
-                                    _t(path, i32, ref, (B, path.shape[1])), _t(accept_len, i32, ref, (B,)),
-                                    _t(next_token, i32, ref, (B,)), _t(status, i32, ref), _raw_stream(stream, ref))
-    _check("dsa_verify_tree", st)
-    return path, accept_len, next_token
+    return (_bound or _binding()).verify_tree(target_probs, draft_probs, tokens, parents, token_start, u_accept, u_sample,
+                                              max_path, path, accept_len, next_token, status, stream)
 
 
 def dsa_cache_compact(caches: dict, block_table, context_lens, token_start, path, accept_len, N=None, keep_lens=None,
@@ -817,26 +718,11 @@ def dsa_cache_compact(caches: dict, block_table, context_lens, token_start, path
     k_cache_scale, v_cache_scale [P, page_size], and kidx_cache with
     kscale_cache where given.  ``N`` bounds token_start (default: none).
     Returns keep_lens int32 [B], the lengths to trim to."""
-    bt = _cuda(block_table)
-    B, max_pages = bt.shape
-    i32, f32 = torch.int32, torch.float32
-    kc, ki, ksc = caches["k_cache"], caches.get("kidx_cache"), caches.get("k_cache_scale")
-    P, ps, d = kc.shape
-    code, slots = torch.bfloat16 if ksc is None else torch.uint8, kc.shape[:2]
-    if keep_lens is None:
-        keep_lens = torch.empty((B,), dtype=i32, device=bt.device)
-    max_path = path.shape[1]
-    d_I = ki.shape[2] if ki is not None else 0
-    with _on(bt):
-        st = load().dsa_cache_compact(
-            _t(bt, i32, bt), _t(context_lens, i32, bt, (B,)), _t(token_start, i32, bt, (B + 1,)),
-            _t(path, i32, bt, (B, max_path)), _t(accept_len, i32, bt, (B,)), B, 2 ** 31 - 1 if N is None else N,
-            max_path, max_pages, P, ps, d_I, d, _t(ki, torch.uint8, bt, (P, ps, d_I)),
-            _t(caches.get("kscale_cache"), f32, bt, slots), _t(kc, code, bt), _t(ksc, f32, bt, slots),
-            _t(caches["v_cache"], code, bt, kc.shape), _t(caches.get("v_cache_scale"), f32, bt, slots),
-            _t(keep_lens, i32, bt, (B,)), _t(status, i32, bt), _raw_stream(stream, bt))
-    _check("dsa_cache_compact", st)
-    return keep_lens
+    get = caches.get
+    return (_bound or _binding()).cache_compact(get("kidx_cache"), get("kscale_cache"), caches["k_cache"],
+                                                get("k_cache_scale"), caches["v_cache"], get("v_cache_scale"),
+                                                block_table, context_lens, token_start, path, accept_len, N, keep_lens,
+                                                status, stream)
 
 
 # Stage names of dsa_profile_read, in dsa_stage order.
