@@ -715,7 +715,7 @@ dsa_status dsa_tree_attn(const void *q, const void *k_cache, const float *k_cach
  * without a change of R and reported.  If R has no positive finite sum,
  * next_token is -1, reported too.
  * status: device uint32_t the caller zeroes beforehand, nullable.  Pointers
- * 16-byte aligned (status 4-byte).  Requires 1 <= V < 2^31, max_path >= 1.  B == 0
+ * 16-byte aligned (status 4-byte).  Requires 1 <= V <= 2^30, max_path >= 1.  B == 0
  * is a no-op; N == 0 needs no rows.
  */
 dsa_status dsa_verify_tree(const float *target_probs, const float *draft_probs, const int32_t *tokens,

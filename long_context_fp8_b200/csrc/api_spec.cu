@@ -13,6 +13,7 @@ inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s
 inline dsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
 constexpr int64_t kInt32Max = 0x7fffffff;
+constexpr int64_t kMaxVocab = 1 << 30;
 
 // Block tables and their pool: shapes shared by the entry points below.
 dsa_status check_pages(int max_pages, int64_t num_pages, int page_size)
@@ -176,7 +177,7 @@ dsa_status dsa_verify_tree(const float *target_probs, const float *draft_probs, 
 {
     if (B < 0 || N < 0 || V < 1 || max_path < 1) return DSA_ERR_INVALID_ARG;
     if (B == 0) return DSA_OK;
-    if (V > kInt32Max || N > kInt32Max || (int64_t)B * 8 > kInt32Max) return DSA_ERR_UNSUPPORTED;
+    if (V > kMaxVocab || N > kInt32Max || (int64_t)B * 8 > kInt32Max) return DSA_ERR_UNSUPPORTED;
     if (!token_start || !u_sample || !path_out || !accept_len || !next_token ||
         (N > 0 && (!target_probs || !tokens || !parents || !u_accept)))
         return DSA_ERR_INVALID_ARG;

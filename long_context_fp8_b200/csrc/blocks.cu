@@ -438,7 +438,7 @@ cudaError_t launch_blocks_extend(const int32_t *new_lens, int32_t *context_lens,
     Maps m{token_start, context_lens, block_table, B, max_pages, ps, num_pages, max_tokens,
            seq_ids, positions, slots, status};
     const bool small = max_tokens <= BL_SMALL;
-    cudaError_t e = launch_cluster(blocks_extend_kernel, 1, small ? 1 : BL_CLUSTER, BL_THREADS, st, new_lens, context_lens,
+    cudaError_t e = launch_cluster(blocks_extend_kernel, 1, small ? 1 : BL_CLUSTER, BL_THREADS, 0, st, new_lens, context_lens,
                                    pages_held, block_table, free_pages, free_capacity, free_count, token_start, m, small);
     if (e != cudaSuccess || small) return e;
     const int64_t need = ceil_div(max_tokens, 4 * BM_THREADS);
@@ -451,7 +451,7 @@ cudaError_t launch_blocks_trim(const int32_t *keep_lens, int32_t *context_lens, 
                                int B, int max_pages, int64_t num_pages, int ps, uint32_t *status, cudaStream_t st)
 {
     const int blocks = (int64_t)B * max_pages <= BL_THREADS ? 1 : BL_CLUSTER;
-    return launch_cluster(blocks_trim_kernel, 1, blocks, BL_THREADS, st, keep_lens, context_lens, pages_held, block_table,
+    return launch_cluster(blocks_trim_kernel, 1, blocks, BL_THREADS, 0, st, keep_lens, context_lens, pages_held, block_table,
                           free_pages, free_capacity, free_count, B, max_pages, num_pages, ps, status);
 }
 

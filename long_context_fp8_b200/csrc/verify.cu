@@ -13,6 +13,8 @@
 // fixed order, so a call repeats bit for bit.  R is never stored: it is made again
 // from P and Q, rejection by rejection, in registers (a node has few rejections, and
 // the second row pass finds P and Q in L2).
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -24,7 +26,9 @@ namespace cg = cooperative_groups;
 
 constexpr int VF_THREADS = 512;
 constexpr int VF_WARPS = VF_THREADS / 32;
-constexpr int VF_STEP = 128;           // elements a warp takes at a time (four a lane)
+constexpr int VF_DEPTH = 6;            // groups of four elements of a lane in the ring
+constexpr int VF_RING = VF_DEPTH * 2 * VF_THREADS * 16;        // bytes: 96 KB, two blocks an SM
+constexpr int VF_CHUNKS = 64;          // parts of a warp's span that the draw looks through
 
 struct VerifyArgs {
     const float *target, *draft;       // draft null: point masses
@@ -45,52 +49,81 @@ struct Residual {
     const double *inv;                 // 1 / Z before each rejection
     const int32_t *gone;               // rejected tokens
     int n;                             // rejections
-    __device__ __forceinline__ double of(float pv, float qv, int64_t v) const
+    __device__ __forceinline__ double of(float pv, float qv, int v) const
     {
         double r = pv;
-        if (q) {
-            for (int k = 0; k < n; ++k) r = positive(r * inv[k] - (double)qv);
-        } else {
-            for (int k = 0; k < n; ++k) r = positive(r * inv[k] - (gone[k] == v ? 1.0 : 0.0));
-        }
+        for (int k = 0; k < n; ++k) r = positive(r * inv[k] - (q ? (double)qv : gone[k] == v ? 1.0 : 0.0));
         return r;
     }
-    __device__ __forceinline__ double at(int64_t v) const { return of(p[v], q ? q[v] : 0.f, v); }
-    // Weights of elements 4 c - skew .. 4 c - skew + 3 (0 outside the row).  `skew`
-    // aligns the 16-byte loads: a row starts at any element.
-    __device__ __forceinline__ void four(int64_t c, int skew, int64_t V, double (&r)[4]) const
+    // Four elements v .. v + 3, from their target and draft values.
+    __device__ __forceinline__ void of4(const float4 &pv, const float4 &qv, int v, double (&r)[4]) const
     {
-        const int64_t v = 4 * c - skew;
-        float pv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f};
-        if (v >= 0 && v + 4 <= V) {
-            const float4 a = *reinterpret_cast<const float4 *>(p + v);
-            pv[0] = a.x; pv[1] = a.y; pv[2] = a.z; pv[3] = a.w;
-            if (q && n > 0) {
-                const float4 b = *reinterpret_cast<const float4 *>(q + v);
-                qv[0] = b.x; qv[1] = b.y; qv[2] = b.z; qv[3] = b.w;
-            }
-        } else {
+        r[0] = pv.x; r[1] = pv.y; r[2] = pv.z; r[3] = pv.w;
+        if (n == 0) return;
+        double qd[4] = {qv.x, qv.y, qv.z, qv.w};
+        double f = inv[0];
+#pragma unroll 1
+        for (int k = 0;;) {
+            if (!q) {
+                const int x = gone[k] - v;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (v + j < 0 || v + j >= V) continue;
-                pv[j] = p[v + j];
-                if (q && n > 0) qv[j] = q[v + j];
+                for (int j = 0; j < 4; ++j) qd[j] = x == j ? 1.0 : 0.0;
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = positive(r[j] * f - qd[j]);
+            if (++k == n) break;
+            f = inv[k];
         }
+    }
+    // Target and draft values of the four elements 4 c - skew .. (0 outside the row).  `skew`
+    // aligns the 16-byte loads: a row starts at any element.
+    __device__ __forceinline__ void load(int c, int skew, int groups, int V, float4 &pv, float4 &qv) const
+    {
+        const int v = 4 * c - skew;
+        qv = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c > 0 && c + 1 < groups) {
+            pv = *reinterpret_cast<const float4 *>(p + v);
+            if (q && n > 0) qv = *reinterpret_cast<const float4 *>(q + v);
+            return;
+        }
+        float a[4], b[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = of(pv[j], qv[j], v + j);
+        for (int j = 0; j < 4; ++j) {
+            const bool in = v + j >= 0 && v + j < V;
+            a[j] = in ? p[v + j] : 0.f;
+            b[j] = in && q && n > 0 ? q[v + j] : 0.f;
+        }
+        pv = make_float4(a[0], a[1], a[2], a[3]);
+        qv = make_float4(b[0], b[1], b[2], b[3]);
+    }
+    __device__ __forceinline__ void four(int c, int skew, int groups, int V, double (&r)[4]) const
+    {
+        float4 pv, qv;
+        load(c, skew, groups, V, pv, qv);
+        of4(pv, qv, 4 * c - skew, r);
     }
 };
 
-__global__ void __launch_bounds__(VF_THREADS)
+__device__ __forceinline__ double warp_sum_of(double s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+__global__ void __launch_bounds__(VF_THREADS, 2)
 verify_tree_kernel(const VerifyArgs a)
 {
+    extern __shared__ float4 ring[];           // [place][target, draft][thread]
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ int32_t parent[DSA_MAX_TREE], token[DSA_MAX_TREE], gone[DSA_MAX_TREE];
-    __shared__ float chance[DSA_MAX_TREE];
+    __shared__ float chance[DSA_MAX_TREE], p_at[DSA_MAX_TREE], q_at[DSA_MAX_TREE];
     __shared__ double inv[DSA_MAX_TREE];
     __shared__ double warp_sum[VF_WARPS];
+    __shared__ double chunk_sum[VF_CHUNKS];
     __shared__ double block_sum[2][8];         // of every block of the cluster, written by them
+    __shared__ int pick;                       // chunk that holds the drawn element, -1: none
+    __shared__ double pick_before;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / blocks;
@@ -111,61 +144,91 @@ verify_tree_kernel(const VerifyArgs a)
         }
         return;
     }
-    const int n = (int)n64;
+    const int n = (int)n64, V = (int)a.V;
     if (tid < n) {
-        parent[tid] = a.parents[t0 + tid];
-        token[tid] = a.tokens[t0 + tid];
+        // the entries that acceptance looks at, all at once: each child's own in its parent's rows
+        const int par = a.parents[t0 + tid], x = a.tokens[t0 + tid];
+        parent[tid] = par;
+        token[tid] = x;
         chance[tid] = a.u_accept[t0 + tid];
+        const bool seen = par >= 0 && par < tid && x >= 0 && x < V;
+        const int64_t at = (t0 + par) * V + x;
+        p_at[tid] = seen ? a.target[at] : 0.f;
+        q_at[tid] = seen && a.draft ? a.draft[at] : 1.f;
     }
+    const double u_sample = a.u_sample[b];
     cluster.sync();                            // every block of the cluster runs: its shared memory may be written
 
-    const int64_t V = a.V;
     int parity = 0;
     Residual R{};
     R.inv = inv;
     R.gone = gone;
-    int skew = 0;
-    int64_t c_begin = 0, c_end = 0;            // this warp's span, in groups of four
+    int skew = 0, groups = 0;
+    int c_begin = 0, c_end = 0;                // this warp's span, in groups of four
     auto move_to = [&](int node) {
         const int64_t at = (t0 + node) * V;
         R.p = a.target + at;
         R.q = a.draft ? a.draft + at : nullptr;
         R.n = 0;
         skew = (int)(at & 3);
-        const int64_t groups = (V + skew + 3) / 4;
-        const int64_t span = ceil_div(groups, (int64_t)blocks * VF_WARPS * (VF_STEP / 4)) * (VF_STEP / 4);
-        c_begin = min(groups, ((int64_t)rank * VF_WARPS + warp) * span);
+        groups = (int)(((int64_t)V + skew + 3) / 4);
+        const int spans = blocks * VF_WARPS;
+        const int span = (groups + spans - 1) / spans;
+        c_begin = min(groups, (rank * VF_WARPS + warp) * span);
         c_end = min(groups, c_begin + span);
     };
     // Sum of R over the row, the same in every thread of the cluster.
     auto sum_row = [&]() -> double {
-        double s0 = 0.0, s1 = 0.0, s2 = 0.0, s3 = 0.0;
-        int64_t c = c_begin + lane;
-        for (; c + 96 < c_end; c += 128) {     // four groups a lane in flight
-            double r0[4], r1[4], r2[4], r3[4];
-            R.four(c, skew, V, r0);
-            R.four(c + 32, skew, V, r1);
-            R.four(c + 64, skew, V, r2);
-            R.four(c + 96, skew, V, r3);
-            s0 += (r0[0] + r0[1]) + (r0[2] + r0[3]);
-            s1 += (r1[0] + r1[1]) + (r1[2] + r1[3]);
-            s2 += (r2[0] + r2[1]) + (r2[2] + r2[3]);
-            s3 += (r3[0] + r3[1]) + (r3[2] + r3[3]);
+        double s0 = 0.0;
+        // The first and last group of the row may be cut: the ring takes the others.  Each lane brings its own
+        // groups into its own places, VF_DEPTH - 1 ahead.
+        const int lo = max(c_begin, 1), hi = min(c_end, groups - 1);
+        const bool two = R.q && R.n > 0;
+        const float *pp = R.p + (4 * (lo + lane) - skew), *qp = two ? R.q + (4 * (lo + lane) - skew) : pp;
+        int left = hi - lo - lane;             // this lane has a group while above 0, and the next every 32
+        constexpr int kPlace = 2 * VF_THREADS; // float4s from one place to the next
+        float4 *const mine = ring + tid;
+#pragma unroll
+        for (int d = 0; d < VF_DEPTH - 1; ++d) {
+            if (left > 32 * d) {
+                cp_async_16(mine + d * kPlace, pp + 128 * d, true);
+                if (two) cp_async_16(mine + d * kPlace + VF_THREADS, qp + 128 * d, true);
+            }
+            cp_async_commit();
         }
-        for (; c < c_end; c += 32) {
+        int v = 4 * (lo + lane) - skew;
+        float4 *now = mine, *then = mine + (VF_DEPTH - 1) * kPlace;    // `then`: read a turn ago
+#pragma unroll 1
+        for (; left > 0; left -= 32, v += 128, pp += 128, qp += 128) {
+            cp_async_wait<VF_DEPTH - 2>();
+            const float4 pv = now[0], qv = now[VF_THREADS];
+            if (left > 32 * (VF_DEPTH - 1)) {
+                cp_async_16(then, pp + 128 * (VF_DEPTH - 1), true);
+                if (two) cp_async_16(then + VF_THREADS, qp + 128 * (VF_DEPTH - 1), true);
+            }
+            cp_async_commit();
+            then = now;
+            now = now == mine + (VF_DEPTH - 1) * kPlace ? mine : now + kPlace;
             double r[4];
-            R.four(c, skew, V, r);
+            R.of4(pv, qv, v, r);
             s0 += (r[0] + r[1]) + (r[2] + r[3]);
         }
-        double s = (s0 + s1) + (s2 + s3);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        cp_async_wait<0>();
+        if (lane < 2) {
+            const int c = lane == 0 ? 0 : groups - 1;
+            if (c >= c_begin && c < c_end && (lane == 0 || groups > 1)) {
+                double r[4];
+                R.four(c, skew, groups, V, r);
+                s0 += (r[0] + r[1]) + (r[2] + r[3]);
+            }
+        }
+        const double s = warp_sum_of(s0);
         if (lane == 0) warp_sum[warp] = s;
         __syncthreads();
-        if (tid == 0) {
+        if (tid < blocks) {
             double t = 0.0;
             for (int w = 0; w < VF_WARPS; ++w) t += warp_sum[w];
-            for (int r = 0; r < blocks; ++r) *cluster.map_shared_rank(&block_sum[parity][rank], r) = t;
+            *cluster.map_shared_rank(&block_sum[parity][rank], tid) = t;
         }
         cluster.sync();
         double t = 0.0;
@@ -187,8 +250,7 @@ verify_tree_kernel(const VerifyArgs a)
                 atomicCAS(a.status, (uint32_t)DSA_OK, (uint32_t)DSA_ERR_INVALID_ARG);
             continue;
         }
-        const double qx = R.q ? (double)R.q[x] : 1.0;
-        if ((double)chance[i] * qx * Z < R.at(x)) {
+        if ((double)chance[i] * (double)q_at[i] * Z < R.of(p_at[i], q_at[i], x)) {
             cur = i;
             move_to(i);
             Z = 1.0;
@@ -215,8 +277,8 @@ verify_tree_kernel(const VerifyArgs a)
     }
     if (!summed) total = sum_row();
 
-    // ---- draw: the block, then the warp, whose span holds the target value
-    const double goal = (double)a.u_sample[b] * total;
+    // ---- draw: the block, the warp's span, then the chunk of it that holds the target value
+    const double goal = u_sample * total;
     const bool drawable = total > 0.0 && total <= 1.7976931348623157e308;
     const int pr = parity ^ 1;
     if (writer) {
@@ -229,35 +291,52 @@ verify_tree_kernel(const VerifyArgs a)
             }
         }
     }
-    if (drawable) {
-        // the first block whose running sum passes the goal; if rounding leaves none, the last with weight
-        int blk = -1, last = 0;
-        double before = 0.0, last_before = 0.0, t = 0.0;
-        for (int r = 0; r < blocks; ++r) {
-            const double s = block_sum[pr][r];
-            if (s > 0.0) { last = r; last_before = t; }
-            if (blk < 0 && t + s > goal) { blk = r; before = t; }
+    // The first of `count` sums that takes the running sum past the goal; if rounding leaves none, the
+    // last with weight.  `before`: the running sum in front of it.
+    auto find = [&](const double *sums, int count, double &before) {
+        int at = -1, last = -1;
+        double t = before, t_at = before, t_last = before;
+        for (int r = 0; r < count && at < 0; ++r) {
+            const double s = sums[r];
+            if (s > 0.0) { last = r; t_last = t; }
+            if (t + s > goal) { at = r; t_at = t; }
             t += s;
         }
-        if (blk < 0) { blk = last; before = last_before; }
-        if (blk == rank) {
-            int w = -1;
-            last = 0;
-            t = last_before = before;
-            double w_before = before;
-            for (int k = 0; k < VF_WARPS; ++k) {
-                const double s = warp_sum[k];
-                if (s > 0.0) { last = k; last_before = t; }
-                if (w < 0 && t + s > goal) { w = k; w_before = t; }
-                t += s;
+        before = at >= 0 ? t_at : t_last;
+        return at >= 0 ? at : last;
+    };
+    if (drawable) {
+        double before = 0.0;
+        if (find(block_sum[pr], blocks, before) == rank) {     // the same in the whole block
+            const int w = find(warp_sum, VF_WARPS, before);
+            const int spans = blocks * VF_WARPS, span = (groups + spans - 1) / spans;
+            const int first = min(groups, (rank * VF_WARPS + w) * span), stop = min(groups, first + span);
+            // its span again, by all warps: sums of chunks of whole warps
+            const int step = 32 * ((span + 32 * VF_CHUNKS - 1) / (32 * VF_CHUNKS));
+            const int chunks = (stop - first + step - 1) / step;
+            for (int k = warp; k < chunks; k += VF_WARPS) {
+                double s = 0.0;
+                for (int c = first + k * step + lane; c < min(stop, first + (k + 1) * step); c += 32) {
+                    double r[4];
+                    R.four(c, skew, groups, V, r);
+                    s += (r[0] + r[1]) + (r[2] + r[3]);
+                }
+                s = warp_sum_of(s);
+                if (lane == 0) chunk_sum[k] = s;
             }
-            if (w < 0) { w = last; w_before = last_before; }
-            if (w == warp) {
-                int64_t found = -1, heaviest = -1;     // heaviest: the last element with weight
-                double run = w_before;
-                for (int64_t c0 = c_begin; c0 < c_end && found < 0; c0 += 32) {
+            __syncthreads();
+            if (tid == 0) {
+                pick = find(chunk_sum, chunks, before);
+                pick_before = before;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                int found = -1, heaviest = -1;                 // heaviest: the last element with weight
+                double run = pick_before;
+                const int from = first + pick * step, to = min(stop, from + step);
+                for (int c0 = from; c0 < to && found < 0; c0 += 32) {
                     double r[4] = {0.0, 0.0, 0.0, 0.0};
-                    if (c0 + lane < c_end) R.four(c0 + lane, skew, V, r);
+                    if (c0 + lane < to) R.four(c0 + lane, skew, groups, V, r);
                     const double mine = (r[0] + r[1]) + (r[2] + r[3]);
                     double upto = mine;
 #pragma unroll
@@ -266,12 +345,12 @@ verify_tree_kernel(const VerifyArgs a)
                         if (lane >= o) upto += p;
                     }
                     // the first weight in this lane that passes the goal, and the last one at all
-                    int64_t hit = -1, any = -1;
+                    int hit = -1, any = -1;
                     double at = run + (upto - mine);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         at += r[j];
-                        const int64_t v = 4 * (c0 + lane) - skew + j;
+                        const int v = 4 * (c0 + lane) - skew + j;
                         if (hit < 0 && r[j] > 0.0 && at > goal) hit = v;
                         if (r[j] > 0.0) any = v;
                     }
@@ -281,7 +360,7 @@ verify_tree_kernel(const VerifyArgs a)
                     if (some) heaviest = __shfl_sync(0xffffffffu, any, 31 - __clz(some));
                     run += __shfl_sync(0xffffffffu, upto, 31);
                 }
-                if (lane == 0) a.next_token[b] = (int32_t)(found >= 0 ? found : heaviest);
+                if (lane == 0) a.next_token[b] = found >= 0 ? found : heaviest;
             }
         }
     }
@@ -297,11 +376,21 @@ cudaError_t launch_verify_tree(const float *target, const float *draft, const in
 {
     const VerifyArgs a{target, draft, tokens, parents, token_start, u_accept, u_sample, N, V, max_path,
                        path, accept_len, next_token, status};
-    // blocks of a sequence: as many as let all of them be resident at once (four of
+    // blocks of a sequence: as many as let all of them be resident at once (two of
     // 512 threads an SM), so that a row is read by as many SMs as there are
+    static std::atomic<uint64_t> ready{0};     // devices whose kernel may use the ring
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(verify_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, VF_RING);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
     int blocks = 8;
-    while (blocks > 1 && (int64_t)B * blocks > 148 * 4) blocks /= 2;
-    return launch_cluster(verify_tree_kernel, (unsigned)B, (unsigned)blocks, VF_THREADS, st, a);
+    while (blocks > 1 && (int64_t)B * blocks > 148 * 2) blocks /= 2;
+    return launch_cluster(verify_tree_kernel, (unsigned)B, (unsigned)blocks, VF_THREADS, VF_RING, st, a);
 }
 
 }  // namespace dsa
