@@ -53,7 +53,7 @@ constexpr int TA_M = 128;              // rows of a tile
 constexpr int TA_BLK = 128;            // cache rows of a block
 constexpr int TA_MAX_CTAS = 160;       // CTAs a workspace has room for (148 SMs)
 constexpr int TA_SEGS = 4;             // segments in the ring
-constexpr int TA_P0 = 6;               // sixteens of a block's weights that P V starts with (of 8)
+constexpr int TA_HALF = 64;            // cache rows of a step of a softmax set
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.f;   // log2 units
@@ -61,7 +61,7 @@ constexpr float kRescaleThreshold = 8.f;   // log2 units
 // Register splits: they add up to the launch's registers only for kernels built with
 // exactly these counts (checked by the build and before every launch).
 constexpr int TA_THREADS = 384, TA_REGS = 168, TA_REGS_LOW = 96, TA_REGS_HIGH = 200;
-constexpr int TA8_THREADS = 512, TA8_REGS = 128, TA8_REGS_LOW = 56, TA8_REGS_HIGH = 200;
+constexpr int TA8_THREADS = 512, TA8_REGS = 128, TA8_REGS_LOW = 88, TA8_REGS_HIGH = 168;
 static_assert(128 * TA_REGS_LOW + 256 * TA_REGS_HIGH <= TA_THREADS * TA_REGS, "register split");
 static_assert(256 * TA8_REGS_LOW + 256 * TA8_REGS_HIGH <= TA8_THREADS * TA8_REGS, "register split");
 
@@ -98,7 +98,7 @@ template <bool KV8, int D> struct Smem {
     static constexpr int q_off = 0;                            // two tiles
     // The (m, l) of both sets lie in Q's second tile, which a single tile leaves free; the
     // next pair's Q waits until they are read.
-    static constexpr int ml_off = q_off + tile;                // [set][m, l][128]
+    static constexpr int ml_off = q_off + tile;                // [item % 2][set][m, l][128]
     static constexpr int kv_off = q_off + 2 * tile;
     static constexpr int code_off = kv_off + slots * tile;
     static constexpr int scale_off = code_off + codes * code_tile;       // KV8: [block % 4][K, V][128]
@@ -106,15 +106,12 @@ template <bool KV8, int D> struct Smem {
     static constexpr int parent_off = mask_off + DSA_MAX_TREE * 16;
     static constexpr int seg_off = parent_off + DSA_MAX_TREE * 2;        // ring of segments
     static constexpr int bar_off = seg_off + TA_SEGS * 48;
-    static constexpr int n_bars = 2 + 2 * slots + 8 + 3 + 2 * TA_SEGS + 2 * codes;
+    static constexpr int n_bars = 2 + 2 * slots + 12 + 4 + 2 * TA_SEGS + 2 * codes;
     static constexpr int ctl_off = bar_off + 8 * n_bars;
     static constexpr int total = ctl_off + 240;
 };
 static_assert(Smem<false, 128>::total <= 232448 && Smem<false, 64>::total <= 232448, "shared memory of a CTA");
 static_assert(Smem<true, 128>::total <= 232448 && Smem<true, 64>::total <= 232448, "shared memory of a CTA");
-
-// A number as a type: for code that must know it when it is compiled.
-template <int N> struct Int { static constexpr int value = N; };
 
 // Control words of a CTA.
 struct Ctl {
@@ -292,15 +289,6 @@ __device__ __forceinline__ int cache_row(const TreeArgs &a, int b, int ctx, int 
     return page * a.page_size + p % a.page_size;
 }
 
-// Four columns of a TMEM row: 128 fp32.
-__device__ __forceinline__ void tmem_row128(uint32_t taddr, uint32_t (&v)[4][32])
-{
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(taddr + c * 32, v[c]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_wait_ld_dep32(v[c]);
-}
-
 template <bool KV8, int D>
 __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                                const CUtensorMap &vmap, const TreeArgs &a)
@@ -310,8 +298,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::bar_off);
     uint64_t *qfull = bars, *qempty = bars + 1, *kvfull = bars + 2, *kvempty = kvfull + SLOTS;
-    uint64_t *sfull = kvempty + SLOTS, *pfull = sfull + 2, *pvdone = pfull + 4, *oempty = pvdone + 2;
-    uint64_t *mfull = oempty + 1, *mempty = mfull + 1, *gfull = mempty + 1, *gempty = gfull + TA_SEGS;
+    uint64_t *sfull = kvempty + SLOTS, *pfull = sfull + 4, *pvdone = pfull + 4, *oempty = pvdone + 4;   // [set][buffer]
+    uint64_t *mfull = oempty + 2, *mempty = mfull + 1, *gfull = mempty + 1, *gempty = gfull + TA_SEGS;
     uint64_t *cfull = gempty + TA_SEGS, *cempty = cfull + CODES;
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::ctl_off);
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask_off);
@@ -335,13 +323,9 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         for (int i = 0; i < SLOTS; ++i) { mbar_init(&kvfull[i], KV8 ? 4 : 1); mbar_init(&kvempty[i], 1); }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[2 * i], 4);
-            mbar_init(&pfull[2 * i + 1], 4);
-            mbar_init(&pvdone[i], 1);
-        }
-        mbar_init(oempty, 8);
+        for (int i = 0; i < 4; ++i) { mbar_init(&sfull[i], 1); mbar_init(&pfull[i], 4); mbar_init(&pvdone[i], 1); }
+        mbar_init(&oempty[0], 8);
+        mbar_init(&oempty[1], 8);
         mbar_init(mfull, 1);
         mbar_init(mempty, 8);
         for (int i = 0; i < TA_SEGS; ++i) { mbar_init(&gfull[i], 1); mbar_init(&gempty[i], KV8 ? 15 : 11); }
@@ -360,6 +344,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     // ---- the CTA's share of the work: a sum over the sequences, then a search
     int64_t all = 0, mine = 0;
     bool any_bad = false;
+#pragma unroll 1
     for (int b = tid; b < a.B; b += threads) {
         Seq s;
         bool bad;
@@ -383,6 +368,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     const int64_t c0 = works ? all * blockIdx.x / ctas : 0, c1 = works ? all * (blockIdx.x + 1) / ctas : 0;
     if (blockIdx.x == 0 && any_bad) ctl->err = DSA_ERR_INVALID_ARG;
     int64_t before = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B && works; b0 += threads) {
         const int b = b0 + tid;
         int64_t c = mine;
@@ -451,10 +437,11 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 int row = cache_row(a, g.b, g.ctx, g.blk0 * TA_BLK + box * a.box, ctl);
                 if (lane == 0) {
                     ok = wait_or_abort(qempty, (item & 1) ^ 1, &ctl->abort);
-                    // every item's end is waited for in turn (a parity tells two phases apart, not
-                    // three); the last item's only where its (m, l) lie in the second tile's place
-                    if (ok && item >= 2) ok = wait_or_abort(oempty, item & 1, &ctl->abort);
-                    if (ok && g.pair && was_single) ok = wait_or_abort(oempty, (item & 1) ^ 1, &ctl->abort);
+                    // the last item's end only where its (m, l) lie in the second tile's place; the one before
+                    // it always, so that no end goes by unseen (a parity tells two phases apart, not three)
+                    if (ok && item >= 2) ok = wait_or_abort(&oempty[item & 1], ((item >> 1) & 1) ^ 1, &ctl->abort);
+                    if (ok && g.pair && was_single)
+                        ok = wait_or_abort(&oempty[(item - 1) & 1], ((item - 1) >> 1) & 1, &ctl->abort);
                     if (ok) {
                         const int tiles = g.pair ? 2 : 1;
                         const int bytes = a.tile_tok * a.rows_tok * 128 * S::halves;
@@ -498,45 +485,45 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         } else if (warp == 1) {
             // ------------------------------------------------ S_x = Q_x K^T
             // (the whole warp keeps step, so that addresses stay in uniform registers; one lane issues)
-            constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, TA_BLK, false);
+            constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, TA_HALF, false);
+            constexpr uint64_t upper = TA_HALF * 128 >> 4;     // the second half's rows of a tile
             const uint64_t qd0 = umma_desc_k_sw128(smem_u32(smem + S::q_off));
             const uint64_t kd0 = umma_desc_k_sw128(smem_u32(smem + S::kv_off));
             Segment g;
-            uint32_t st = 0, ph = 0, cnt[2] = {0, 0};  // slot and its phase; products of each set
+            uint32_t st = 0, ph = 0, cnt = 0;          // slot and its phase; steps of each set
             int item = 0;
             bool ok = true;
-            auto product = [&](auto xc, uint64_t qd, uint64_t kd) {
-                constexpr int x = decltype(xc)::value;
-                // P_x lies in S_x: the last P V of the set must have read it
-                ok = __all_sync(0xffffffffu, ok && wait_or_abort(&pvdone[x], (cnt[x] & 1) ^ 1, &ctl->abort));
+            auto product = [&](int x, uint32_t k, uint64_t qd, uint64_t kd) {
+                const uint32_t buf = k & 1;
+                // P lies in S: the P V of two steps ago must have read it
+                ok = __all_sync(0xffffffffu, ok && wait_or_abort(&pvdone[2 * x + buf], ((k >> 1) & 1) ^ 1, &ctl->abort));
                 if (!ok) return;
                 tc_fence_after();
                 if (elect_sync()) {
+                    const uint32_t d = tS + x * 128 + buf * TA_HALF;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         constexpr int h = S::half >> 4;
-                        umma_f16(tS + x * 128, qd + (kk >> 2) * h + (kk & 3) * 2, kd + (kk >> 2) * h + (kk & 3) * 2, idesc,
+                        umma_f16(d, qd + (kk >> 2) * h + (kk & 3) * 2, kd + (kk >> 2) * h + (kk & 3) * 2, idesc,
                                  kk > 0 ? 1u : 0u);
                     }
-                    umma_commit(&sfull[x]);
-                    ctl->s_issued[x] = (int)cnt[x] + 1;
+                    umma_commit(&sfull[2 * x + buf]);
+                    ctl->s_issued[x] = (int)k + 1;
                 }
                 __syncwarp();
-                ++cnt[x];
             };
             for (; ok && next(g); ++item) {
                 ok = __all_sync(0xffffffffu, wait_or_abort(qfull, item & 1, &ctl->abort));
                 for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
                     ok = __all_sync(0xffffffffu, wait_or_abort(&kvfull[st], ph, &ctl->abort));
                     const uint64_t kd = kd0 + (uint64_t)(st * (S::tile >> 4));
-                    if (g.pair) {
-                        product(Int<0>{}, qd0, kd);
-                        product(Int<1>{}, qd0 + (S::tile >> 4), kd);
-                    } else if (((blk - g.blk0) & 1) == 0) {
-                        product(Int<0>{}, qd0, kd);
-                    } else {
-                        product(Int<1>{}, qd0, kd);
+                    // a pair: both tiles by each half of the rows; a single tile: its set for each half
+#pragma unroll 1
+                    for (int u = 0; u < (g.pair ? 4 : 2); ++u) {
+                        const int x = u & 1, h = g.pair ? u >> 1 : u;
+                        product(x, cnt + (g.pair ? h : 0), qd0 + (g.pair && x ? S::tile >> 4 : 0), kd + (h ? upper : 0));
                     }
+                    cnt += g.pair ? 2 : 1;
                     if (ok && elect_sync()) umma_commit(&kvempty[st]);
                     __syncwarp();
                     st += 2;
@@ -550,46 +537,39 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             constexpr uint32_t idesc = umma_idesc_bf16_f32(TA_M, D, true);
             const uint64_t vd0 = umma_desc_mn_sw128(smem_u32(smem + S::kv_off), S::half, 1024);
             Segment g;
-            uint32_t st = 1, ph = 0, cnt[2] = {0, 0};
+            uint32_t st = 1, ph = 0, cnt = 0;
             int item = 0;
             bool ok = true;
-            auto product = [&](auto xc, uint64_t vd, bool first) {
-                constexpr int x = decltype(xc)::value;
-                // most of the columns as soon as their weights are there
+            constexpr uint64_t upper = TA_HALF * 128 >> 4;
+            auto product = [&](int x, uint32_t k, uint64_t vd, bool first) {
+                const uint32_t buf = k & 1;
+                ok = __all_sync(0xffffffffu, ok && wait_or_abort(&pfull[2 * x + buf], (k >> 1) & 1, &ctl->abort));
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_sync()) {
+                    const uint32_t pa = tS + x * 128 + buf * TA_HALF;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    ok = __all_sync(0xffffffffu, ok && wait_or_abort(&pfull[2 * x + h], cnt[x] & 1, &ctl->abort));
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (elect_sync()) {
-#pragma unroll
-                        for (int kk = h * TA_P0; kk < (h ? TA_BLK / 16 : TA_P0); ++kk)
-                            umma_f16_ts(tO + x * 128, tS + x * 128 + kk * 8, vd + kk * 128, idesc,
-                                        (first && kk == 0) ? 0u : 1u);
-                        if (h == 1) {
-                            umma_commit(&pvdone[x]);
-                            ctl->pv_issued[x] = (int)cnt[x] + 1;
-                        }
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < TA_HALF / 16; ++kk)
+                        umma_f16_ts(tO + x * 128, pa + kk * 8, vd + kk * 128, idesc, (first && kk == 0) ? 0u : 1u);
+                    umma_commit(&pvdone[2 * x + buf]);
+                    ctl->pv_issued[x] = (int)k + 1;
                 }
-                ++cnt[x];
+                __syncwarp();
             };
             for (; ok && next(g); ++item) {
                 // the item before has read its O
-                ok = __all_sync(0xffffffffu, wait_or_abort(oempty, (item & 1) ^ 1, &ctl->abort));
+                if (item > 0)
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&oempty[(item - 1) & 1], ((item - 1) >> 1) & 1, &ctl->abort));
                 for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
                     ok = __all_sync(0xffffffffu, wait_or_abort(&kvfull[st], ph, &ctl->abort));
                     const uint64_t vd = vd0 + (uint64_t)(st * (S::tile >> 4));
-                    const int nth = blk - g.blk0;
-                    if (g.pair) {
-                        product(Int<0>{}, vd, nth == 0);
-                        product(Int<1>{}, vd, nth == 0);
-                    } else if ((nth & 1) == 0) {
-                        product(Int<0>{}, vd, nth < 2);
-                    } else {
-                        product(Int<1>{}, vd, nth < 2);
+                    const bool first = blk == g.blk0;
+#pragma unroll 1
+                    for (int u = 0; u < (g.pair ? 4 : 2); ++u) {
+                        const int x = u & 1, h = g.pair ? u >> 1 : u;
+                        product(x, cnt + (g.pair ? h : 0), vd + (h ? upper : 0), first && u < 2);
                     }
+                    cnt += g.pair ? 2 : 1;
                     if (ok && elect_sync()) umma_commit(&kvempty[st]);
                     __syncwarp();
                     st += 2;
@@ -720,10 +700,11 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         const int r = tid & 127;                   // row of the tile
         const uint32_t trow = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tSx = tS + x * 128 + trow, tOx = tO + x * 128 + trow;
-        float *ml = reinterpret_cast<float *>(smem + S::ml_off);
         const int tr = r / a.rows_tok, hr = r - tr * a.rows_tok;
         Segment g;
-        uint32_t cnt[2] = {0, 0}, i0 = 0;          // products of each set; blocks before this segment
+        uint32_t cnt = 0, i0 = 0;                  // steps of each set and blocks, before this segment
+        uint32_t items = 0;                        // segments before this one
+        uint32_t singles = 0;                      // items of a single tile before this one
         int cur = -1, seqs = 0;                    // sequence, and how many before it
         bool masked = false;                       // its masks are there
         bool dead = false;
@@ -753,37 +734,44 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             const bool valid = tr < a.tile_tok && tok < s.n && head < a.group;
             const int node = valid ? tok : 0;
             const int nb = g.blk1 - g.blk0;
-            const int step = g.pair ? 1 : 2, b_first = g.pair ? g.blk0 : g.blk0 + x;
+            // a pair: both halves of every block; a single tile: the set's own half
+            const int steps = g.pair ? 2 * nb : nb;
             float m = -INFINITY, l = 0.f;
-            uint32_t k = cnt[x];
-            for (int blk = b_first; blk < g.blk1 && !dead; blk += step, ++k) {
-                const uint32_t i = i0 + (blk - g.blk0), tv = 2 * i + 1, stv = tv % SLOTS;
-                bool ok = wait_or_abort(&sfull[x], k & 1, &ctl->abort);
+            for (int t = 0; t < steps && !dead; ++t) {
+                const uint32_t k = cnt + t, buf = k & 1;
+                const int nth = g.pair ? t >> 1 : t, half = g.pair ? t & 1 : x;
+                const int pos = (g.blk0 + nth) * TA_BLK + half * TA_HALF;      // the step's first position
+                const uint32_t i = i0 + nth, tv = 2 * i + 1, stv = tv % SLOTS;
+                const uint32_t tSb = tSx + buf * TA_HALF;
+                bool ok = wait_or_abort(&sfull[2 * x + buf], (k >> 1) & 1, &ctl->abort);
                 // V's tile (and the scales of K and V with it)
-                const bool tail = (blk + 1) * TA_BLK > s.ctx;
+                const bool tail = pos + TA_HALF > s.ctx;
                 if (KV8 || tail) ok = ok && wait_or_abort(&kvfull[stv], (tv / SLOTS) & 1, &ctl->abort);
                 if (!__all_sync(0xffffffffu, ok)) { dead = true; break; }
                 tc_fence_after();
-                uint32_t v[4][32];
-                tmem_row128(tSx, v);
+                uint32_t v[2][32];
+                tmem_ld32(tSb, v[0]);
+                tmem_ld32(tSb + 32, v[1]);
+                tmem_wait_ld_dep32(v[0]);
+                tmem_wait_ld_dep32(v[1]);
+                const float4 *sc = reinterpret_cast<const float4 *>(scales + (i & 3) * 256 + half * TA_HALF);
                 if (KV8) {
-                    const float4 *sc = reinterpret_cast<const float4 *>(scales + (i & 3) * 256);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
+                    for (int c = 0; c < 16; ++c) {
                         const float4 f = sc[c];
                         uint32_t *u = &v[c >> 3][(c & 7) * 4];
                         f2_scale(u[0], u[1], f.x, f.y);
                         f2_scale(u[2], u[3], f.z, f.w);
                     }
                 }
-                if ((blk + 1) * TA_BLK > prefix) {
-                    // the drafts (and what lies behind them): column c is draft j = blk 128 + c - prefix
+                if (pos + TA_HALF > prefix) {
+                    // the drafts (and what lies behind them): column c is draft j = pos + c - prefix
                     need_masks();
                     if (dead) break;
                     const uint32_t *mw = masks + 4 * node;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int j0 = blk * TA_BLK + c * 32 - prefix;
+                    for (int c = 0; c < 2; ++c) {
+                        const int j0 = pos + c * 32 - prefix;
                         uint32_t bits;
                         if (j0 <= -32) bits = 0xffffffffu;
                         else if (j0 < 0) bits = (mw[0] << -j0) | ((1u << -j0) - 1u);
@@ -796,7 +784,9 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                     if (!KV8 && tail) {
                         // V's rows behind the context, up to the end of their box, may hold anything:
                         // their weights are 0, but 0 times an infinity is not
-                        const int lo = s.ctx - blk * TA_BLK, hi = (lo + a.box - 1) / a.box * a.box;
+                        const int ctx_row = s.ctx - (g.blk0 + nth) * TA_BLK;
+                        const int lo = max(ctx_row, half * TA_HALF);
+                        const int hi = min((ctx_row + a.box - 1) / a.box * a.box, (half + 1) * TA_HALF);
                         uint8_t *vt = smem + S::kv_off + stv * S::tile;
                         for (int q = r; q < (hi - lo) * S::halves * 8; q += 128) {
                             const int row = lo + q / (S::halves * 8), c = q % (S::halves * 8);
@@ -808,20 +798,25 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 }
                 float mx[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(v[q][0]);
+                for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(v[c >> 1][(c & 1) * 16]);
 #pragma unroll
-                for (int q = 1; q < 31; q += 2)
+                for (int q = 1; q < 15; q += 2)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(v[c][q]), __uint_as_float(v[c][q + 1]));
+                    for (int c = 0; c < 4; ++c)
+                        mx[c] = max3(mx[c], __uint_as_float(v[c >> 1][(c & 1) * 16 + q]),
+                                     __uint_as_float(v[c >> 1][(c & 1) * 16 + q + 1]));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][31]));
+                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(v[c >> 1][(c & 1) * 16 + 15]));
                 const float mr = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 const float mb = mr * a.scale_log2;            // the scale is positive
                 const bool grows = mb > m + kRescaleThreshold || (m == -INFINITY && mb != -INFINITY);
-                // tcgen05.ld/st take the whole warp; the last P V of this set is done (S waited for it)
                 if (__any_sync(0xffffffffu, grows)) {
                     const float f = grows ? (m == -INFINITY ? 0.f : exp2f(m - mb)) : 1.f;
-                    if (blk > b_first) {
+                    if (t > 0) {
+                        // the last step's P V must be done; tcgen05.ld/st take the whole warp
+                        ok = wait_or_abort(&pvdone[2 * x + (buf ^ 1)], ((k - 1) >> 1) & 1, &ctl->abort);
+                        if (!__all_sync(0xffffffffu, ok)) { dead = true; break; }
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
@@ -839,32 +834,22 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nb2 = f2_pack(-base, -base);
                 const uint64_t one2 = f2_pack(1.f, 1.f);
                 uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-                const float4 *vs4 = reinterpret_cast<const float4 *>(scales + (i & 3) * 256 + 128);
+                uint32_t pk[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {                  // 32 columns: 16 words of P
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const uint32_t *u = &v[c][2 * q];
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), sc2, nb2), x0, x1);
-                        float p0 = ex2_sfu(x0), p1 = ex2_sfu(x1);
-                        rs2[q & 3] = f2_fma(f2_pack(p0, p1), one2, rs2[q & 3]);
-                        if (KV8) {
-                            const float4 f = vs4[c * 8 + (q >> 1)];
-                            f2_unpack(f2_mul(f2_pack(p0, p1), (q & 1) ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y)), p0, p1);
-                        }
-                        pk[q] = pack_bf16x2(p0, p1);           // the products' precision: one rounding of each weight
+                for (int q = 0; q < 32; ++q) {
+                    const uint32_t *u = &v[q >> 4][(2 * q) & 31];
+                    float p0, p1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(u[0]), __uint_as_float(u[1])), sc2, nb2), p0, p1);
+                    p0 = ex2_sfu(p0);
+                    p1 = ex2_sfu(p1);
+                    rs2[q & 3] = f2_fma(f2_pack(p0, p1), one2, rs2[q & 3]);
+                    if (KV8) {
+                        const float4 f = sc[32 + (q >> 1)];
+                        f2_unpack(f2_mul(f2_pack(p0, p1), (q & 1) ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y)), p0, p1);
                     }
-                    tmem_st16(tSx + c * 16, pk);
-                    if (c >= 2) {
-                        static_assert(TA_P0 == 6, "three of four stores come before P V starts");
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pfull[2 * x + c - 2]);
-                    }
+                    pk[q] = pack_bf16x2(p0, p1);               // the products' precision: one rounding of each weight
                 }
+                tmem_st32(tSb, pk);
                 float rsum = 0.f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -873,27 +858,31 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                     rsum += lo + hi;
                 }
                 l += rsum;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[2 * x + buf]);
             }
             // ---- the item's end (or this CTA's part of it)
-            const int n0 = g.pair ? nb : (nb + 1) / 2, n1 = g.pair ? nb : nb / 2;
-            cnt[0] += n0;
-            cnt[1] += n1;
+            cnt += steps;
             i0 += nb;
             need_masks();
             const uint32_t *mw = masks + 4 * node;
             const bool lives = valid && !dead && ((mw[node >> 5] >> (node & 31)) & 1u);
-            if (!lives) l = 0.f;                   // a padding row: zeros and -inf
+            if (!lives || m == -INFINITY) l = 0.f;                   // a padding row: zeros and -inf
             float m_o = -INFINITY, l_o = 0.f;      // the other set's part of the row
             if (!g.pair) {
+                // two copies in turn: a set may be an item ahead of the other, which still reads
+                float *ml = reinterpret_cast<float *>(smem + S::ml_off) + (singles++ & 1) * 512;
                 ml[x * 256 + r] = m;
                 ml[x * 256 + 128 + r] = l;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 m_o = ml[(x ^ 1) * 256 + r];
                 l_o = ml[(x ^ 1) * 256 + 128 + r];
-                if (!dead && x == 1 && n0 > 0 && !wait_or_abort(&pvdone[0], (cnt[0] - 1) & 1, &ctl->abort)) dead = true;
-                if (!dead && x == 0 && n1 > 0 && !wait_or_abort(&pvdone[1], (cnt[1] - 1) & 1, &ctl->abort)) dead = true;
+                // (both sets have taken the same steps)
+                if (!dead && !wait_or_abort(&pvdone[2 * (x ^ 1) + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1, &ctl->abort)) dead = true;
             }
-            if (!dead && (x == 0 ? n0 : n1) > 0 && !wait_or_abort(&pvdone[x], (cnt[x] - 1) & 1, &ctl->abort)) dead = true;
+            if (!dead && !wait_or_abort(&pvdone[2 * x + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1, &ctl->abort)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) {
                 __syncwarp();
@@ -912,20 +901,16 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + g.hk * a.group + head;
             // a single tile: set x takes half of the columns of both parts
             const int col0 = g.pair ? 0 : x * (D / 2), cols = g.pair ? D : D / 2;
-            const bool have_own = (x == 0 ? n0 : n1) > 0, have_oth = !g.pair && (x == 0 ? n1 : n0) > 0;
             const uint32_t tOo = tO + (x ^ 1) * 128 + trow;
+#pragma unroll 1
             for (int c = col0; c < col0 + cols; c += 32) {
                 uint32_t o[32];
                 float acc[32];
+                tmem_ld32(tOx + c, o);
+                tmem_wait_ld_dep32(o);
 #pragma unroll
-                for (int q = 0; q < 32; ++q) acc[q] = 0.f;
-                if (have_own) {
-                    tmem_ld32(tOx + c, o);
-                    tmem_wait_ld_dep32(o);
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) acc[q] = __uint_as_float(o[q]) * g_own;
-                }
-                if (have_oth) {
+                for (int q = 0; q < 32; ++q) acc[q] = __uint_as_float(o[q]) * g_own;
+                if (!g.pair) {
                     tmem_ld32(tOo + c, o);
                     tmem_wait_ld_dep32(o);
 #pragma unroll
@@ -959,7 +944,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             tc_fence_before();
             fence_proxy_async_smem();              // ml, before TMA may write Q there
             __syncwarp();
-            if (lane == 0) mbar_arrive(oempty);
+            if (lane == 0) mbar_arrive(&oempty[items & 1]);
+            ++items;
         }
     }
 
@@ -974,8 +960,9 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 mbar_wait(KV8 ? &cfull[j % ring] : &kvfull[j % ring], (j / ring) & 1);
             if (ctl->q_issued > 0) mbar_wait(qfull, (ctl->q_issued - 1) & 1);
             for (int y = 0; y < 2; ++y) {
-                if (ctl->s_issued[y] > 0) mbar_wait(&sfull[y], (ctl->s_issued[y] - 1) & 1);
-                if (ctl->pv_issued[y] > 0) mbar_wait(&pvdone[y], (ctl->pv_issued[y] - 1) & 1);
+                const int ns = ctl->s_issued[y] - 1, np = ctl->pv_issued[y] - 1;
+                if (ns >= 0) mbar_wait(&sfull[2 * y + (ns & 1)], (ns >> 1) & 1);
+                if (np >= 0) mbar_wait(&pvdone[2 * y + (np & 1)], (np >> 1) & 1);
             }
         }
         a.err[blockIdx.x] = (uint32_t)ctl->err;
