@@ -453,6 +453,25 @@ def test_tree_attn_many_sequences(B):
 
 
 @pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_attn_many_short_items(d, kv8):
+    """Several items a CTA, single tiles and pairs in turn, some of one block: the sets' steps, the item ends
+    and the statistics of one item must not be taken for another's."""
+    rng = np.random.default_rng(19)
+    ns = [int(v) for v in rng.choice([0, 1, 2, 3, 4, 5, 7], 700)]
+    ctxs = [n + int(rng.choice([0, 3, 60, 130, 300], p=[0.3, 0.3, 0.2, 0.1, 0.1])) for n in ns]
+    inp, vals = _tree_case(rng, ns, ctxs, 64, 1, d, 32, kv8)
+    ws = dsa.workspace(dsa.tree_attn_workspace_size(700, sum(ns), 64, 1, d), "cuda")
+    out, lse = torch.full((sum(ns), 64, d), 9.0, dtype=torch.bfloat16, device="cuda"), torch.full((sum(ns), 64), 9.0, device="cuda")
+    for _ in range(5):
+        _run_tree(inp, out=out, lse=lse, ws=ws)
+        assert dsa.dsa_stream_status(ws) == 0
+    _check_tree(inp, vals, out, lse, d ** -0.5, [b for b in range(700) if ns[b] and b % 7 == 0])
+    again, lse2 = _run_tree(inp)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
 def test_tree_attn_far_into_a_large_cache(kv8):
     """Pages whose elements lie past 2^31 of a cache."""
     rng = np.random.default_rng(17)
