@@ -36,7 +36,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-r
 # many registers per thread, so any other count fails the build (instead of a
 # launch that would wait forever in setmaxnreg, or a silent slower path).
 SETMAXNREG_KERNELS = {"index_tc_kernel": 168, "sparse_attn_tc_kernel": 168, "tree_attn_kernel": 168,
-                      "tree_attn_kv8_kernel": 128}
+                      "tree_attn_kv8_kernel": 96}
 
 
 def kernel_name(mangled: str) -> str:

@@ -12,29 +12,41 @@
 // dim 128 also 1024.
 //
 // The work of a launch is one list: sequence by sequence, K/V head by head, pair of
-// row tiles by pair, its blocks of cache rows.  A block costs 2 for a pair of tiles and
-// 1 for a single one, and each CTA (one per SM) takes an equal share of the list,
-// wherever it begins and ends: no length or batch leaves SMs idle, and a single long
-// sequence spreads over all of them.  An item (row tiles of one sequence and head) that
-// is cut leaves partial results (fp32 O / l and log-sum-exp), which a second, chained kernel
-// merges; the others are written at once.
+// row tiles by pair, its blocks of cache rows, each at the cost that was measured for
+// it.  Each CTA (one per SM) takes an equal share of the list, wherever it begins and
+// ends: no length or batch leaves SMs idle, and a single long sequence spreads over all
+// of them.  An item (row tiles of one sequence and head) that is cut leaves partial
+// results (fp32 O / l and log-sum-exp), which a second, chained kernel merges; the
+// others are written at once.
 //
-// Roles of a CTA (first warpgroup), bf16:
+// Roles of a CTA, bf16:
 //   warp 0  brings Q and the K and V tiles by TMA through the page table, one box
 //           of gcd(page_size, 128) rows a page, into a ring of 32 KB slots; boxes behind the
 //           context (and pages out of range) start behind the cache's last row, which
 //           TMA fills with zeros;
-//   warp 1  issues S_x = Q_x K^T into TMEM, x = 0, 1;
+//   warp 1  issues S_x = Q_x K^T into TMEM, x = 0, 1, 64 cache rows at a time;
 //   warp 2  issues O_x += P_x V, P_x from TMEM;
-//   warp 3  walks the tree and leaves each token's ancestors as 128 bits.
-// With FP8 caches a fourth warpgroup widens the E4M3 codes to bf16 (exactly) into the
-// ring; the scales stay in fp32 and multiply the logits and the weights.
-//   warpgroups 1 and 2 are softmax sets, a thread a row: set x takes tile x of
-//           a pair, or every other block of a single tile (merged at the end).  P
-//           takes the place of S in TMEM, so a set alternates with its own MMAs while the
-//           other set's run.  O is rescaled only where the maximum grows by more
-//           than 2^8, which is exact up to rounding.
+//   warp 3  walks the list of work, and the tree of each sequence: each token's ancestors
+//           as 128 bits;
+//   warps 4-7 and 8-11 are softmax sets, a thread a row: set x takes tile x of a pair
+//           (both halves of each block) or half x of each block of a single tile (merged at
+//           the end).  Each set has two score buffers in TMEM, so that the next scores
+//           are made while it works; P takes the place of S.  O is rescaled only where the
+//           maximum grows by more than 2^8, which is exact up to rounding.
+// With FP8 caches warp 0 brings codes, and eight more warps (12-15: K, 16-19: V) widen
+// them to bf16, exactly, into the ring; the scales stay in fp32 and multiply the logits
+// and the weights.
 // Every mbarrier wait is bounded (DSA_ERR_TIMEOUT on expiry).
+//
+// Measured on one B200 (6.55 TB/s and 1.40 PFLOP/s sustained): 16 x 64K contexts, 8-16
+// drafts, 128 heads on one K/V head 0.56 ms back to back (1.1 PFLOP/s, 79 % of the sustained rate: the clock
+// falls to 1.7 GHz under the power limit, and half of the exponentials on the FMA pipe took
+// 15 % fewer clocks but more power, and so more time); 64 x 32K, one draft, pages of
+// 128 rows 145 us (5.5 TB/s, 84 %; with pages of 16 rows, whose boxes are 2 KB, 4.2); FP8 64 x 32K x
+// 2-3 drafts 0.33 ms, bound by the widening and by shared memory, which the products,
+// the widening and the scales share.  The code of the hot roles has to fit the
+// instruction cache: one copy of each product's code instead of four took the FP8
+// kernel from 450 to 358 us.  128-row steps over one score buffer: bf16 585, FP8 432 us.
 #include <algorithm>
 #include <atomic>
 #include <numeric>
@@ -61,9 +73,9 @@ constexpr float kRescaleThreshold = 8.f;   // log2 units
 // Register splits: they add up to the launch's registers only for kernels built with
 // exactly these counts (checked by the build and before every launch).
 constexpr int TA_THREADS = 384, TA_REGS = 168, TA_REGS_LOW = 96, TA_REGS_HIGH = 200;
-constexpr int TA8_THREADS = 512, TA8_REGS = 128, TA8_REGS_LOW = 88, TA8_REGS_HIGH = 168;
+constexpr int TA8_THREADS = 640, TA8_REGS = 96, TA8_REGS_LOW = 56, TA8_REGS_HIGH = 152;
 static_assert(128 * TA_REGS_LOW + 256 * TA_REGS_HIGH <= TA_THREADS * TA_REGS, "register split");
-static_assert(256 * TA8_REGS_LOW + 256 * TA8_REGS_HIGH <= TA8_THREADS * TA8_REGS, "register split");
+static_assert(384 * TA8_REGS_LOW + 256 * TA8_REGS_HIGH <= TA8_THREADS * TA8_REGS, "register split");
 
 struct TreeArgs {
     const uint16_t *q;
@@ -108,7 +120,7 @@ template <bool KV8, int D> struct Smem {
     static constexpr int bar_off = seg_off + TA_SEGS * 48;
     static constexpr int n_bars = 2 + 2 * slots + 12 + 4 + 2 * TA_SEGS + 2 * codes;
     static constexpr int ctl_off = bar_off + 8 * n_bars;
-    static constexpr int total = ctl_off + 240;
+    static constexpr int total = ctl_off + 256;
 };
 static_assert(Smem<false, 128>::total <= 232448 && Smem<false, 64>::total <= 232448, "shared memory of a CTA");
 static_assert(Smem<true, 128>::total <= 232448 && Smem<true, 64>::total <= 232448, "shared memory of a CTA");
@@ -122,9 +134,9 @@ struct Ctl {
     long long start_base;              // work before that sequence
     long long c0, c1;                  // the CTA's share of the work
     int kv_issued, q_issued, code_issued, s_issued[2], pv_issued[2];
-    long long sums[16];
+    long long sums[20];
 };
-static_assert(sizeof(Ctl) <= 240, "control words");
+static_assert(sizeof(Ctl) <= 256, "control words");
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
@@ -328,7 +340,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         mbar_init(&oempty[1], 8);
         mbar_init(mfull, 1);
         mbar_init(mempty, 8);
-        for (int i = 0; i < TA_SEGS; ++i) { mbar_init(&gfull[i], 1); mbar_init(&gempty[i], KV8 ? 15 : 11); }
+        for (int i = 0; i < TA_SEGS; ++i) { mbar_init(&gfull[i], 1); mbar_init(&gempty[i], KV8 ? 19 : 11); }
         if (KV8)
             for (int i = 0; i < CODES; ++i) { mbar_init(&cfull[i], 1); mbar_init(&cempty[i], 4); }
         ctl->abort = 0;
@@ -635,66 +647,67 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 ++seq;
             }
         } else if (KV8) {
-            // ------------------------------------------------ E4M3 -> bf16 (warps 12-15)
-            // Every E4M3 value is a bf16 value.  Thread i brings the two scales of
+            // ------------------------------------------------ E4M3 -> bf16 (warps 12-15: K, 16-19: V)
+            // Every E4M3 value is a bf16 value.  Thread i of the V warps brings the two scales of
             // row i of a block, a block ahead (their addresses go through the page table).
-            const int ct = tid - 384;
+            const int ct = tid & 127, kv = (warp >> 2) - 3;
             Segment g;
-            uint32_t t = 0, i = 0;
+            uint32_t t = kv, i = 0;
             bool ok = true;
             while (ok && next(g)) {
-                const Segment &s = g;
-                const int64_t none = a.num_pages * a.page_size;
-                auto row_of = [&](int blk) -> int64_t {
-                    return blk < g.blk1 ? cache_row(a, g.b, s.ctx, blk * TA_BLK + ct, ctl) : none;
+                const int none = (int)(a.num_pages * a.page_size);
+                auto row_of = [&](int blk) {
+                    return kv && blk < g.blk1 ? cache_row(a, g.b, g.ctx, blk * TA_BLK + ct, ctl) : none;
                 };
-                auto scale_of = [&](const float *p, int64_t r) { return r < none ? p[r * a.Hkv + g.hk] : 0.f; };
-                int64_t r1 = row_of(g.blk0);
+                auto scale_of = [&](const float *p, int r) { return r < none ? p[(int64_t)r * a.Hkv + g.hk] : 0.f; };
+                int r1 = row_of(g.blk0);
                 float ksc = scale_of(a.ks, r1), vsc = scale_of(a.vs, r1);
                 r1 = row_of(g.blk0 + 1);
-                for (int blk = g.blk0; ok && blk < g.blk1; ++blk, ++i) {
+#pragma unroll 1
+                for (int blk = g.blk0; blk < g.blk1; ++blk, ++i, t += 2) {
                     const float k_now = ksc, v_now = vsc;
                     ksc = scale_of(a.ks, r1);
                     vsc = scale_of(a.vs, r1);
                     r1 = row_of(blk + 2);
-                    for (int kv = 0; kv < 2; ++kv, ++t) {
-                        const uint32_t cs = t % CODES, st = t % SLOTS;
-                        ok = wait_or_abort(&cfull[cs], (t / CODES) & 1, &ctl->abort) &&
-                             wait_or_abort(&kvempty[st], ((t / SLOTS) & 1) ^ 1, &ctl->abort);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        scales[(i & 3) * 256 + kv * 128 + ct] = kv ? v_now : k_now;
-                        const uint8_t *src = smem + S::code_off + cs * S::code_tile;
-                        uint8_t *dst = smem + S::kv_off + st * S::tile;
+                    const uint32_t cs = t % CODES, st = t % SLOTS;
+                    ok = wait_or_abort(&cfull[cs], (t / CODES) & 1, &ctl->abort) &&
+                         wait_or_abort(&kvempty[st], ((t / SLOTS) & 1) ^ 1, &ctl->abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (kv) {
+                        scales[(i & 3) * 256 + ct] = k_now;
+                        scales[(i & 3) * 256 + 128 + ct] = v_now;
+                    }
+                    const uint8_t *src = smem + S::code_off + cs * S::code_tile;
+                    uint8_t *dst = smem + S::kv_off + st * S::tile;
 #pragma unroll 1
-                        for (int j0 = 0; j0 < D / 16; j0 += 2) {
-                            // reads before writes: the compiler cannot know that they are apart
-                            uint4 raw[2];
+                    for (int j0 = 0; j0 < D / 16; j0 += 2) {
+                        // reads before writes: the compiler cannot know that they are apart
+                        uint4 raw[2];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) raw[j] = *reinterpret_cast<const uint4 *>(src + ((ct + 128 * (j0 + j)) << 4));
+                        for (int j = 0; j < 2; ++j) raw[j] = *reinterpret_cast<const uint4 *>(src + ((ct + 128 * (j0 + j)) << 4));
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int q = ct + 128 * (j0 + j), row = q / (D / 16), c = q % (D / 16);
-                                // rows behind the context count as zeros, whatever they hold
-                                if (blk * TA_BLK + row >= s.ctx) raw[j] = make_uint4(0u, 0u, 0u, 0u);
-                                uint32_t o[8];
-                                e4m3x16_to_bf16(raw[j], o);
-                                uint8_t *p = dst + (c >> 2) * S::half + row * 128;
-                                const int c0 = (c & 3) * 2;
-                                // the two halves of a row start on the same banks: the upper one's threads
-                                // write their chunks in the other order
-                                const int f = c >> 2;
-                                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                                *reinterpret_cast<uint4 *>(p + (((c0 + f) ^ (row & 7)) << 4)) = f ? hi : lo;
-                                *reinterpret_cast<uint4 *>(p + (((c0 + 1 - f) ^ (row & 7)) << 4)) = f ? lo : hi;
-                            }
+                        for (int j = 0; j < 2; ++j) {
+                            const int q = ct + 128 * (j0 + j), row = q / (D / 16), c = q % (D / 16);
+                            // rows behind the context count as zeros, whatever they hold
+                            if (blk * TA_BLK + row >= g.ctx) raw[j] = make_uint4(0u, 0u, 0u, 0u);
+                            uint32_t o[8];
+                            e4m3x16_to_bf16(raw[j], o);
+                            uint8_t *p = dst + (c >> 2) * S::half + row * 128;
+                            const int c0 = (c & 3) * 2;
+                            // the two halves of a row start on the same banks: the upper one's threads
+                            // write their chunks in the other order
+                            const int f = c >> 2;
+                            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                            *reinterpret_cast<uint4 *>(p + (((c0 + f) ^ (row & 7)) << 4)) = f ? hi : lo;
+                            *reinterpret_cast<uint4 *>(p + (((c0 + 1 - f) ^ (row & 7)) << 4)) = f ? lo : hi;
                         }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&kvfull[st]);
-                            mbar_arrive(&cempty[cs]);
-                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&kvfull[st]);
+                        mbar_arrive(&cempty[cs]);
                     }
                 }
             }
@@ -1187,9 +1200,9 @@ cudaError_t launch_tree_attn(const uint16_t *q, const void *k, const float *ks, 
     a.rows_tok = std::min(a.group, TA_M);
     a.tile_tok = TA_M / a.rows_tok;
     a.head_tiles = (int)ceil_div(a.group, TA_M);
-    // measured a block: bf16 2.1 us for a pair and 1.3 for one, FP8 3.1 and 2.3 (the conversion is the same)
-    a.cost_pair = ks ? 4 : 5;
-    a.cost_one = 3;
+    // measured a block: bf16 2.1 us for a pair and 1.3 for one, FP8 3.1 and 2.2 (the conversion is the same)
+    a.cost_pair = ks ? 7 : 5;
+    a.cost_one = ks ? 5 : 3;
     a.scale_log2 = sm_scale * kLog2e;
     a.out = out;
     a.lse = lse;
