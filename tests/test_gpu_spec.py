@@ -914,3 +914,49 @@ def test_calls_on_tensors_of_a_stream():
     dsa.dsa_rope(x, pos, table, q_out=out, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(out, dsa.dsa_rope(x, pos, table)[0])
+
+
+def test_binding_refusals():
+    """What the binding checks before the library sees it: types, shapes, layouts and places of the tensors."""
+    rng = np.random.default_rng(23)
+    inp, _ = _tree_case(rng, [3, 2], [40, 20], 8, 2, 64, 16, False)
+    dev = {k: v.cuda() for k, v in inp.items()}
+    N = 5
+    for change in (dict(q=dev["q"].half()), dict(q=dev["q"][:, ::2]), dict(q=inp["q"]), dict(q=dev["q"][0]),
+                   dict(k_cache=dev["k_cache"][..., :32].contiguous()), dict(v_cache=dev["v_cache"][:-1].contiguous()),
+                   dict(v_cache=dev["v_cache"].float()), dict(block_table=dev["block_table"].long()),
+                   dict(context_lens=inp["context_lens"]), dict(token_start=dev["token_start"][:-1].contiguous()),
+                   dict(parents=dev["parents"][1:].contiguous()), dict(k_cache_scale=torch.ones(3, device="cuda")),
+                   dict(q=None)):
+        with pytest.raises(ValueError):
+            dsa.dsa_tree_attn({**dev, **change}, 3, 40)
+    for kw in (dict(out=torch.empty_like(dev["q"])[:-1]), dict(out=torch.empty(N, 8, 64, device="cuda")),
+               dict(lse=torch.empty(N, 7, device="cuda")), dict(ws=torch.empty(1 << 22, device="cuda"))):
+        with pytest.raises(ValueError):
+            dsa.dsa_tree_attn(dev, 3, 40, **kw)
+    for kw in (dict(sm_scale=float("nan")), dict(ws=torch.empty(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(dsa.DSAError):
+            dsa.dsa_tree_attn(dev, 3, 40, **kw)
+    with pytest.raises(ValueError):
+        dsa.dsa_tree_attn(dev, 2 ** 40, 40)                  # does not fit the C argument
+    x, pos, table = torch.randn(4, 2, 64, device="cuda"), _dev(np.arange(4)), dsa.dsa_rope_freqs(64)
+    for args, kw in (((x.double(), pos, table), {}), ((x, pos[:3], table), {}), ((x, pos.long(), table), {}),
+                     ((x.transpose(0, 1), pos[:2], table), {}), ((x, pos, table), dict(k=x[:3])),
+                     ((x, pos, table), dict(k=x.bfloat16())), ((x, pos, table), dict(q_out=x[:, :1])),
+                     ((x, pos, table), dict(k=x, k_out=x.cpu()))):
+        with pytest.raises(ValueError):
+            dsa.dsa_rope(*args, **kw)
+    P, i = torch.full((3, 10), 0.1, device="cuda"), _dev(np.zeros(3))
+    good = [P, None, i, _dev([-1, 0, 1]), _dev([0, 3]), torch.rand(3, device="cuda"), torch.rand(1, device="cuda")]
+    for at, bad in ((0, P.half()), (0, P[0]), (1, P[:, :9].contiguous()), (2, i[:2]), (3, i.long()), (4, i[:1]),
+                    (5, P[0, :2].contiguous()), (6, P)):
+        with pytest.raises(ValueError):
+            dsa.dsa_verify_tree(*[bad if k == at else v for k, v in enumerate(good)])
+    with pytest.raises(ValueError):
+        dsa.dsa_verify_tree(*good, max_path=4, path=torch.empty((1, 5), dtype=torch.int32, device="cuda"))
+    pool = dict(block_table=_dev(np.zeros((2, 4))), context_lens=_dev([0, 0]), pages_held=_dev([0, 0]),
+                free_pages=_dev([1, 2]), free_count=_dev([2]))
+    for change in (dict(block_table=_dev(np.zeros(8))), dict(context_lens=_dev([0])), dict(free_count=_dev([2, 2])),
+                   dict(free_pages=torch.zeros(4, device="cuda"))):
+        with pytest.raises(ValueError):
+            dsa.dsa_blocks_trim({**pool, **change}, _dev([0, 0]), 16)
