@@ -1015,6 +1015,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 //   out = sum_i 2^(L_i - M) O_i / sum_i 2^(L_i - M),  L_i the parts' log2 sums.
 constexpr int TM_THREADS = 256;        // rows of two tiles
 constexpr int TM_QUADS = 4;            // sixteen columns: 32 bytes of output, a sector
+constexpr int TM_PARTS = 4;            // parts in flight
 
 template <int D>
 __global__ void __launch_bounds__(TM_THREADS)
@@ -1051,20 +1052,24 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
         }
     }
     __syncthreads();
-    // a block per item and TM_QUADS column quads, a thread per row
+    // a block per item and TM_QUADS column quads, a thread per row; a single tile has 128 rows, and the
+    // threads behind them take every other part
     constexpr int groups = D / 4 / TM_QUADS;
+    __shared__ float4 half_acc[TM_QUADS][128];
+    __shared__ float2 half_ml[128];
     for (int u = blockIdx.x; u < n_items * groups; u += gridDim.x) {
-        const int c = first[u / groups], quad = (u % groups) * TM_QUADS, row = tid;
+        const int c = first[u / groups], quad = (u % groups) * TM_QUADS;
         const int4 d = desc[c];
         Seq s;
         bool bad;
         s.load(a, d.x, bad);
-        const int x = row >> 7, r = row & 127;
-        if (x == 1 && !(d.w & 2)) continue;
+        const bool pair = d.w & 2;
+        const int x = pair ? tid >> 7 : 0, r = tid & 127, row = x * 128 + r;
+        const int step = pair ? 1 : 2, begin = pair ? 0 : tid >> 7;
         const int tile = d.z + x, tr = r / a.rows_tok;
         const int tok = (a.head_tiles > 1 ? tile / a.head_tiles : tile * a.tile_tok) + tr;
         const int head = (a.head_tiles > 1 ? (tile % a.head_tiles) * TA_M : 0) + r - tr * a.rows_tok;
-        if (tr >= a.tile_tok || tok >= s.n || head >= a.group) continue;
+        const bool valid = tr < a.tile_tok && tok < s.n && head < a.group;
         int parts = 1;
         while (c + parts - 1 < ctas && (desc[c + parts - 1].w & 1) && same(c, c + parts - 1)) ++parts;
         // part 0: slot 1 of CTA c - 1; part p: slot 0 of CTA c - 1 + p
@@ -1075,18 +1080,21 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
         float4 acc[TM_QUADS];
 #pragma unroll
         for (int e = 0; e < TM_QUADS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = 0; p0 < parts; p0 += 4) {
-            float L[4];
-            float4 o[4][TM_QUADS];
+        for (int p0 = begin; valid && p0 < parts; p0 += TM_PARTS * step) {
+            float L[TM_PARTS];
+            float4 o[TM_PARTS][TM_QUADS];
+            float top = M;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < TM_PARTS; ++q) {
                 L[q] = -INFINITY;
-                if (p0 + q >= parts) continue;
-                L[q] = a.part_lse[at(p0 + q) * 256 + row];
+                const int p = p0 + q * step;
+                if (p >= parts) continue;
+                L[q] = a.part_lse[at(p) * 256 + row];
 #pragma unroll
-                for (int e = 0; e < TM_QUADS; ++e) o[q][e] = part[at(p0 + q) * (D / 4 * 256) + e * 256];
+                for (int e = 0; e < TM_QUADS; ++e) o[q][e] = part[at(p) * (D / 4 * 256) + e * 256];
             }
-            const float top = fmaxf(fmaxf(fmaxf(L[0], L[1]), fmaxf(L[2], L[3])), M);
+#pragma unroll
+            for (int q = 0; q < TM_PARTS; ++q) top = fmaxf(top, L[q]);
             if (top == -INFINITY) continue;
             const float f = exp2f(M - top);
             M = top;
@@ -1099,8 +1107,8 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
                 acc[e].w *= f;
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (p0 + q >= parts) continue;
+            for (int q = 0; q < TM_PARTS; ++q) {
+                if (p0 + q * step >= parts) continue;
                 const float wt = exp2f(L[q] - M);
                 sum += wt;
 #pragma unroll
@@ -1112,6 +1120,30 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
                 }
             }
         }
+        if (!pair) {
+            if (begin == 1) {
+#pragma unroll
+                for (int e = 0; e < TM_QUADS; ++e) half_acc[e][r] = acc[e];
+                half_ml[r] = make_float2(M, sum);
+            }
+            __syncthreads();
+            if (begin == 0) {
+                const float2 other = half_ml[r];
+                const float top = fmaxf(M, other.x);
+                const float f0 = M == -INFINITY ? 0.f : exp2f(M - top), f1 = other.x == -INFINITY ? 0.f : exp2f(other.x - top);
+                M = top;
+                sum = sum * f0 + other.y * f1;
+#pragma unroll
+                for (int e = 0; e < TM_QUADS; ++e) {
+                    const float4 b = half_acc[e][r];
+                    acc[e] = make_float4(acc[e].x * f0 + b.x * f1, acc[e].y * f0 + b.y * f1, acc[e].z * f0 + b.z * f1,
+                                         acc[e].w * f0 + b.w * f1);
+                }
+            }
+            __syncthreads();                   // half_acc may be written again
+            if (begin == 1) continue;
+        }
+        if (!valid) continue;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + d.y * a.group + head;
         uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * D + quad * 4);
