@@ -909,9 +909,10 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             }
             tc_fence_after();
             const float mt = fmaxf(l > 0.f ? m : -INFINITY, l_o > 0.f ? m_o : -INFINITY);
-            const float f_own = l > 0.f ? exp2f(m - mt) : 0.f, f_oth = l_o > 0.f ? exp2f(m_o - mt) : 0.f;
+            // (a sum that is no number, from a query that is none, stays one)
+            const float f_own = l != 0.f ? exp2f(m - mt) : 0.f, f_oth = l_o != 0.f ? exp2f(m_o - mt) : 0.f;
             const float lt = l * f_own + l_o * f_oth;
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const float inv = lt != 0.f ? 1.f / lt : 0.f;
             const float g_own = f_own * inv, g_oth = f_oth * inv;
             const bool whole = g.blk0 == 0 && g.blk1 == s.nblk;
             // slot 0: an item that began in an earlier CTA, 1: one that ends in a later CTA
@@ -956,9 +957,9 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 }
             }
             if (valid && (g.pair || x == 0)) {
-                const float l2 = lives && lt > 0.f ? mt + log2f(lt) : -INFINITY;
+                const float l2 = lives && lt != 0.f ? mt + log2f(lt) : -INFINITY;
                 if (!whole) a.part_lse[pslot * 256 + prow] = l2;
-                else if (a.lse) a.lse[orow] = lives && lt > 0.f ? mt * kLn2 + logf(lt) : -INFINITY;
+                else if (a.lse) a.lse[orow] = lives && lt != 0.f ? mt * kLn2 + logf(lt) : -INFINITY;
             }
             tc_fence_before();
             fence_proxy_async_smem();              // ml, before TMA may write Q there
@@ -1084,6 +1085,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
             float L[TM_PARTS];
             float4 o[TM_PARTS][TM_QUADS];
             float top = M;
+            bool any = false;                  // a part that holds something, if only a NaN
 #pragma unroll
             for (int q = 0; q < TM_PARTS; ++q) {
                 L[q] = -INFINITY;
@@ -1094,9 +1096,12 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
                 for (int e = 0; e < TM_QUADS; ++e) o[q][e] = part[at(p) * (D / 4 * 256) + e * 256];
             }
 #pragma unroll
-            for (int q = 0; q < TM_PARTS; ++q) top = fmaxf(top, L[q]);
-            if (top == -INFINITY) continue;
-            const float f = exp2f(M - top);
+            for (int q = 0; q < TM_PARTS; ++q) {
+                top = fmaxf(top, L[q]);
+                any |= L[q] != -INFINITY;
+            }
+            if (!any) continue;
+            const float f = sum != 0.f ? exp2f(M - top) : 0.f;
             M = top;
             sum *= f;
 #pragma unroll
@@ -1109,7 +1114,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
 #pragma unroll
             for (int q = 0; q < TM_PARTS; ++q) {
                 if (p0 + q * step >= parts) continue;
-                const float wt = exp2f(L[q] - M);
+                const float wt = L[q] != -INFINITY ? exp2f(L[q] - M) : 0.f;
                 sum += wt;
 #pragma unroll
                 for (int e = 0; e < TM_QUADS; ++e) {
@@ -1130,7 +1135,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
             if (begin == 0) {
                 const float2 other = half_ml[r];
                 const float top = fmaxf(M, other.x);
-                const float f0 = M == -INFINITY ? 0.f : exp2f(M - top), f1 = other.x == -INFINITY ? 0.f : exp2f(other.x - top);
+                const float f0 = sum != 0.f ? exp2f(M - top) : 0.f, f1 = other.y != 0.f ? exp2f(other.x - top) : 0.f;
                 M = top;
                 sum = sum * f0 + other.y * f1;
 #pragma unroll
@@ -1144,7 +1149,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
             if (begin == 1) continue;
         }
         if (!valid) continue;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
         const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + d.y * a.group + head;
         uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * D + quad * 4);
 #pragma unroll
@@ -1152,7 +1157,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
             out[e / 2] = make_uint4(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv),
                                     pack_bf16x2(acc[e + 1].x * inv, acc[e + 1].y * inv),
                                     pack_bf16x2(acc[e + 1].z * inv, acc[e + 1].w * inv));
-        if (quad == 0 && a.lse) a.lse[orow] = sum > 0.f ? M * kLn2 + logf(sum) : -INFINITY;
+        if (quad == 0 && a.lse) a.lse[orow] = sum != 0.f ? M * kLn2 + logf(sum) : -INFINITY;
     }
 }
 

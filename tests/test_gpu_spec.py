@@ -428,6 +428,25 @@ def test_tree_attn_bad_pages_count_as_zero_rows(kv8):
         _check_tree(inp, z, out, lse, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("ns,ctxs", [([4, 3], [100, 60]), ([4, 3], [3000, 2000]), ([40], [5000])])
+def test_tree_attn_a_query_that_is_no_number_stays_in_its_row(ns, ctxs):
+    rng = np.random.default_rng(24)
+    for kv8 in (False, True):
+        inp, vals = _tree_case(rng, ns, ctxs, 16, 1, 128, 64, kv8)
+        want, want_lse = _run_tree(inp)
+        inp["parents"][2] = -2                               # a padding row
+        base, base_lse = _run_tree(inp)
+        bad = dict(inp, q=inp["q"].clone())
+        bad["q"][1, 3, 5], bad["q"][2], bad["q"][0, 0, 0] = float("nan"), float("nan"), float("inf")
+        out, lse = _run_tree(bad)
+        assert torch.isnan(out[1, 3]).all() and torch.isnan(lse[1, 3])
+        assert torch.all(out[2] == 0) and torch.isneginf(lse[2]).all()
+        keep = torch.ones(sum(ns), 16, dtype=torch.bool)
+        keep[1, 3] = keep[0, 0] = False
+        assert torch.equal(out[keep], base[keep]) and torch.equal(lse[keep], base_lse[keep])
+        assert not torch.isnan(want).any() and not torch.isnan(want_lse).any()
+
+
 def test_tree_attn_rows_behind_the_last_sequence_stay():
     rng = np.random.default_rng(16)
     inp, vals = _tree_case(rng, [3, 2], [130, 64], 16, 1, 128, 64, False)
