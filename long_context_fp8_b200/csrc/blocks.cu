@@ -257,9 +257,11 @@ blocks_trim_kernel(const int32_t *keep_lens, int32_t *context_lens, int32_t *pag
         stay = (int)min(held, (keep + ps - 1) / ps);
         return held - stay;
     };
-    // first round: how many pages come back in all (the first of them goes on top)
+    // first round: how many pages come back in all (the first of them goes on top); a single chunk
+    // knows it when it has summed
     int64_t asked = 0, all = 0;
-    for (int b0 = 0; b0 < B; b0 += BL_THREADS) {
+    const bool one = B <= BL_THREADS;
+    for (int b0 = 0; b0 < B && !one; b0 += BL_THREADS) {
         const int b = b0 + tid;
         int stay = 0;
         const int64_t freed = b < B ? max((int64_t)0, freed_of(b, stay)) : 0;
@@ -269,7 +271,7 @@ blocks_trim_kernel(const int32_t *keep_lens, int32_t *context_lens, int32_t *pag
         if (asked > room) block_scan({upto > room ? 0 : freed, 0}, sums, &total);
         all += total.a;
     }
-    cluster.sync();                    // all have read free_count
+    if (!one) cluster.sync();          // all have read free_count
     asked = 0;
     int64_t before = 0;
     for (int b0 = 0; b0 < B; b0 += BL_THREADS) {
@@ -291,6 +293,7 @@ blocks_trim_kernel(const int32_t *keep_lens, int32_t *context_lens, int32_t *pag
             }
             end = block_scan({max((int64_t)0, freed), 0}, sums, &total).a;
         }
+        if (one) all = total.a;
         ends[tid] = end;
         first_page[tid] = stay;
         cluster.sync();                // all have read this chunk's lengths; and the block its shared arrays
