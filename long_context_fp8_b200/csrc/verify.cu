@@ -1,18 +1,25 @@
 // Verification of drafted token trees against the target's probabilities.
 //
 // Along the walk almost nothing is read: a child is accepted or rejected on one
-// entry of its parent's target and draft rows.  Only a rejection sums a whole row
-// (Z = sum_v max(R(v) / Z - Q(v), 0)), and the last one is drawn from.  So a
-// sequence reads, besides single entries, one pair of rows for each rejection, or
-// the last node's target row alone if no child was left to reject.
+// entry of its parent's target and draft rows, and these are read all at once. Only a
+// rejection sums a whole row (Z = sum_v max(R(v) / Z - Q(v), 0)), and the last one is
+// drawn from.  So a sequence reads, besides single entries, one pair of rows for each
+// rejection, or the last node's target row alone if no child was left to reject; with point
+// masses one row for the first rejection and one for the draw, since the others change one entry.
 //
 // A cluster of thread blocks takes a sequence.  Every block runs the same walk from
 // the same values; a row is cut into contiguous spans, one a warp, and each warp
 // sums its span in 64 bits.  The warps' sums are kept: the draw finds the span by
-// their running sum and only that warp goes through its span again.  Sums have a
-// fixed order, so a call repeats bit for bit.  R is never stored: it is made again
-// from P and Q, rejection by rejection, in registers (a node has few rejections, and
-// the second row pass finds P and Q in L2).
+// their running sum, the block goes through that span again in chunks, and one warp
+// through the chunk that holds the value.  Sums have a fixed order, so a call repeats bit
+// for bit.  R is never stored: it is made again from P and Q, rejection by rejection, in
+// registers (a node has few rejections, and the second row pass finds P and Q in L2).
+//
+// Measured on one B200: a chain of 5 over 32 000 tokens 7.8 us; 64 trees of 16 over
+// 128 001 tokens 44 us (121 at first, with 125 registers: one block an SM, four waves of
+// clusters), of which the sequence with four rejections takes 8 us a pass: 100
+// instructions for four elements a lane, most of them the 64-bit arithmetic, bind it on its four
+// SMs, not the bytes (32 in flight a thread or 192 made no difference there).
 #include <atomic>
 
 #include <cooperative_groups.h>
