@@ -319,6 +319,9 @@ TREE_CASES = [
     ([9], [700], 128, 1, 128, 64),
     ([2, 3], [500, 130], 256, 1, 128, 128),          # a token takes two tiles
     ([2], [333], 200, 1, 64, 16),                    # and the second of them is not full
+    ([3, 2], [200, 70], 300, 1, 64, 16),             # three tiles a token: a pair holds two tokens' tiles
+    ([2, 1], [150, 40], 512, 4, 128, 16),            # one full tile a token
+    ([5, 3], [260, 33], 100, 1, 128, 32),            # 28 rows of every tile that no head has
     ([33, 64, 1], [100, 64, 900], 40, 1, 128, 16),
     ([128, 127], [128, 400], 4, 4, 64, 32),          # the largest trees
     ([5, 6], [1000, 70], 48, 16, 128, 64),           # groups of 3: 42 tokens and 2 rows that no token has
