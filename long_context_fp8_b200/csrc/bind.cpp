@@ -11,6 +11,7 @@
 #include <string>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -122,17 +123,37 @@ uint32_t *status_word(PyObject *o, const Tensor &ref)
     return o == Py_None ? nullptr : (uint32_t *)address(o, at::kInt, ref);
 }
 
-// A stream object, or None: the current stream of ref's device.
-void *as_stream(PyObject *o, const Tensor &ref)
-{
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(ref.get_device()).stream();
-    PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
-    if (!v) throw Raised{};
-    void *s = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
-    if (!s && PyErr_Occurred()) throw Raised{};
-    return s;
-}
+// The device and stream of a call: a stream object's, or with None the current
+// one.  What the call allocates belongs to that stream: memory from another
+// stream's pool may still be in use there, and a workspace would go back to that
+// pool while the call runs.  Outputs go to the caller, whose current stream is
+// told of them.
+struct Run {
+    c10::cuda::CUDAGuard device;
+    c10::cuda::CUDAStream caller;
+    c10::cuda::OptionalCUDAStreamGuard other;
+    void *stream;
+
+    Run(PyObject *o, const Tensor &ref)
+        : device(ref.device()), caller(c10::cuda::getCurrentCUDAStream(ref.get_device())), stream(caller.stream())
+    {
+        if (o == Py_None) return;
+        PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
+        if (!v) throw Raised{};
+        stream = PyLong_AsVoidPtr(v);
+        Py_DECREF(v);
+        if (!stream && PyErr_Occurred()) throw Raised{};
+        if (stream != caller.stream())
+            other.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)stream, ref.get_device()));
+    }
+
+    Tensor output(at::IntArrayRef sizes, const at::TensorOptions &options) const
+    {
+        Tensor t = at::empty(sizes, options);
+        if (other.current_stream()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), caller);
+        return t;
+    }
+};
 
 void done(const char *fn, dsa_status st)
 {
@@ -191,12 +212,12 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded([&]() -> PyObject * {
         arguments(n, 12);
         const Tensor &q = reference(a[0]);
-        c10::cuda::CUDAGuard device(q.device());
+        const Run run(a[11], q);
         const ScalarType type = q.scalar_type();
         if (type != at::kBFloat16 && type != at::kFloat) throw Bad("dsa_rope takes bf16 or fp32");
         const int64_t qs = rope_stride(q, nullptr);
         const int64_t rows = q.size(0), d = q.size(2);
-        const Tensor q_out = a[9] == Py_None ? at::empty(q.sizes(), q.options()) : as_tensor(a[9]);
+        const Tensor q_out = a[9] == Py_None ? run.output(q.sizes(), q.options()) : as_tensor(a[9]);
         const int64_t qos = rope_stride(q_out, &q);
         Tensor k_out;
         const void *kp = nullptr;
@@ -208,7 +229,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
             H_k = k.size(1);
             if (k.size(0) != rows || k.size(2) != d || k.scalar_type() != type || k.device() != q.device())
                 throw Bad("q and k must agree in rows, head dimension, type and device");
-            k_out = a[10] == Py_None ? at::empty(k.sizes(), k.options()) : as_tensor(a[10]);
+            k_out = a[10] == Py_None ? run.output(k.sizes(), k.options()) : as_tensor(a[10]);
             kos = rope_stride(k_out, &k);
             kp = k.data_ptr();
             kop = k_out.data_ptr();
@@ -218,7 +239,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
                                     (const int32_t *)address(a[2], at::kInt, q, {rows}), rows, (int)d, as_int32(a[5]),
                                     as_int32(a[4]), as_bool(a[6]), (const uint64_t *)as_int(a[3]), (float)as_double(a[7]),
                                     as_bool(a[8]), q_out.data_ptr(), qos, kop, kos,
-                                    type == at::kBFloat16 ? DSA_BF16 : DSA_F32, as_stream(a[11], q)));
+                                    type == at::kBFloat16 ? DSA_BF16 : DSA_F32, run.stream));
         return Py_BuildValue("NN", keep(a[9], q_out), a[1] == Py_None ? Py_NewRef(Py_None) : keep(a[10], k_out));
     });
 }
@@ -249,7 +270,7 @@ PyObject *blocks_extend(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded([&]() -> PyObject * {
         arguments(n, 15);
         const Pool p(a);
-        c10::cuda::CUDAGuard device(p.table.device());
+        const Run run(a[14], p.table);
         const int64_t m = as_int(a[8]);
         done("dsa_blocks_extend",
              g_lib.blocks_extend((const int32_t *)address(a[5], at::kInt, p.table, {p.B}), p.context_lens, p.pages_held,
@@ -258,7 +279,7 @@ PyObject *blocks_extend(PyObject *, PyObject *const *a, Py_ssize_t n)
                                  (int32_t *)address(a[10], at::kInt, p.table, {m}),
                                  (int32_t *)address(a[11], at::kInt, p.table, {m}),
                                  (int64_t *)optional(a[12], at::kLong, p.table, {m}), status_word(a[13], p.table),
-                                 as_stream(a[14], p.table)));
+                                 run.stream));
         Py_RETURN_NONE;
     });
 }
@@ -269,11 +290,11 @@ PyObject *blocks_trim(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded([&]() -> PyObject * {
         arguments(n, 10);
         const Pool p(a);
-        c10::cuda::CUDAGuard device(p.table.device());
+        const Run run(a[9], p.table);
         done("dsa_blocks_trim",
              g_lib.blocks_trim((const int32_t *)address(a[5], at::kInt, p.table, {p.B}), p.context_lens, p.pages_held,
                                p.block_table, p.free_pages, p.capacity, p.free_count, (int)p.B, (int)p.width, as_int(a[7]),
-                               as_int32(a[6]), status_word(a[8], p.table), as_stream(a[9], p.table)));
+                               as_int32(a[6]), status_word(a[8], p.table), run.stream));
         Py_RETURN_NONE;
     });
 }
@@ -285,7 +306,7 @@ PyObject *tree_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded([&]() -> PyObject * {
         arguments(n, 16);
         const Tensor &q = reference(a[0]), &kc = as_tensor(a[1]), &bt = as_tensor(a[5]);
-        c10::cuda::CUDAGuard device(q.device());
+        const Run run(a[15], q);
         if (q.dim() != 3 || bt.dim() != 2 || (kc.dim() != 3 && kc.dim() != 4))
             throw Bad("expected q [N, H_q, d], block_table [B, max_pages] and caches [P, page_size(, H_kv), d]");
         const int64_t N = q.size(0), H = q.size(1), d = q.size(2), B = bt.size(0);
@@ -297,8 +318,8 @@ PyObject *tree_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
         const bool kv8 = a[2] != Py_None;
         const ScalarType code = kv8 ? at::kByte : at::kBFloat16;
         const at::IntArrayRef scales = kc.sizes().slice(0, kc.dim() - 1);
-        const Tensor out = a[12] == Py_None ? at::empty(q.sizes(), q.options()) : as_tensor(a[12]);
-        const Tensor lse = a[13] == Py_None ? at::empty({N, H}, q.options().dtype(at::kFloat)) : as_tensor(a[13]);
+        const Tensor out = a[12] == Py_None ? run.output(q.sizes(), q.options()) : as_tensor(a[12]);
+        const Tensor lse = a[13] == Py_None ? run.output({N, H}, q.options().dtype(at::kFloat)) : as_tensor(a[13]);
         Tensor ws = a[14] == Py_None ? Tensor() : as_tensor(a[14]);
         if (!ws.defined())
             ws = at::empty({(int64_t)g_lib.tree_attn_workspace_size((int)B, N, (int)H, (int)Hkv, (int)d) + 256},
@@ -319,7 +340,7 @@ PyObject *tree_attn(PyObject *, PyObject *const *a, Py_ssize_t n)
                              (const int32_t *)address(a[8], at::kInt, q, {N}), kc.size(0), (int)bt.size(1),
                              (int)kc.size(1), (int)B, N, as_int32(a[9]), as_int(a[10]), (int)H, (int)Hkv, (int)d, sm,
                              out.data_ptr(), (float *)lse.data_ptr(), ws.data_ptr(), (size_t)ws.numel(),
-                             as_stream(a[15], q)));
+                             run.stream));
         return Py_BuildValue("NN", keep(a[12], out), keep(a[13], lse));
     });
 }
@@ -330,17 +351,17 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded([&]() -> PyObject * {
         arguments(n, 13);
         const Tensor &p = reference(a[0]), &us = as_tensor(a[6]);
-        c10::cuda::CUDAGuard device(p.device());
+        const Run run(a[12], p);
         if (p.dim() != 2 || us.dim() != 1) throw Bad("expected target_probs [N, V] and u_sample [B]");
         const int64_t N = p.size(0), V = p.size(1), B = us.size(0);
         if (B > INT32_MAX) throw Bad("dsa_verify_tree: a size is out of range");
         const auto ints = p.options().dtype(at::kInt);
-        const Tensor path = a[8] == Py_None ? at::empty({B, a[7] == Py_None ? DSA_MAX_TREE : as_int(a[7])}, ints)
+        const Tensor path = a[8] == Py_None ? run.output({B, a[7] == Py_None ? DSA_MAX_TREE : as_int(a[7])}, ints)
                                             : as_tensor(a[8]);
         if (path.dim() != 2 || path.size(0) != B || path.size(1) > INT32_MAX) throw Bad("expected path [B, max_path]");
         if (a[8] != Py_None && a[7] != Py_None && as_int(a[7]) != path.size(1)) throw Bad("path's width is max_path");
-        const Tensor len = a[9] == Py_None ? at::empty({B}, ints) : as_tensor(a[9]);
-        const Tensor next = a[10] == Py_None ? at::empty({B}, ints) : as_tensor(a[10]);
+        const Tensor len = a[9] == Py_None ? run.output({B}, ints) : as_tensor(a[9]);
+        const Tensor next = a[10] == Py_None ? run.output({B}, ints) : as_tensor(a[10]);
         for (const Tensor *t : {&path, &len, &next}) check(*t, at::kInt, p);
         if (len.numel() != B || next.numel() != B) throw Bad("expected accept_len and next_token [B]");
         done("dsa_verify_tree",
@@ -352,7 +373,7 @@ PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n)
                                (const float *)address(a[5], at::kFloat, p, {N}),
                                (const float *)address(a[6], at::kFloat, p), (int)B, N, V, (int)path.size(1),
                                (int32_t *)path.data_ptr(), (int32_t *)len.data_ptr(), (int32_t *)next.data_ptr(),
-                               status_word(a[11], p), as_stream(a[12], p)));
+                               status_word(a[11], p), run.stream));
         return Py_BuildValue("NNN", keep(a[8], path), keep(a[9], len), keep(a[10], next));
     });
 }
@@ -364,7 +385,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded([&]() -> PyObject * {
         arguments(n, 15);
         const Tensor &bt = reference(a[6]), &kc = as_tensor(a[2]), &path = as_tensor(a[9]);
-        c10::cuda::CUDAGuard device(bt.device());
+        const Run run(a[14], bt);
         if (bt.dim() != 2 || kc.dim() != 3 || path.dim() != 2)
             throw Bad("expected block_table [B, max_pages], caches [P, page_size, d] and path [B, max_path]");
         const int64_t B = bt.size(0), P = kc.size(0), ps = kc.size(1), d = kc.size(2), m = path.size(1);
@@ -377,7 +398,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (B > INT32_MAX || bt.size(1) > INT32_MAX || ps > INT32_MAX || d > INT32_MAX || m > INT32_MAX || d_I > INT32_MAX)
             throw Bad("dsa_cache_compact: a size is out of range");
         const ScalarType code = a[3] == Py_None ? at::kBFloat16 : at::kByte;
-        const Tensor lens = a[12] == Py_None ? at::empty({B}, bt.options()) : as_tensor(a[12]);
+        const Tensor lens = a[12] == Py_None ? run.output({B}, bt.options()) : as_tensor(a[12]);
         check(lens, at::kInt, bt);
         if (lens.numel() != B) throw Bad("expected keep_lens [B]");
         done("dsa_cache_compact",
@@ -391,7 +412,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *a, Py_ssize_t n)
                                  (float *)optional(a[1], at::kFloat, bt, {P, ps}), address(a[2], code, bt),
                                  (float *)optional(a[3], at::kFloat, bt, {P, ps}), address(a[4], code, bt, kc.sizes()),
                                  (float *)optional(a[5], at::kFloat, bt, {P, ps}), (int32_t *)lens.data_ptr(),
-                                 status_word(a[13], bt), as_stream(a[14], bt)));
+                                 status_word(a[13], bt), run.stream));
         return keep(a[12], lens);
     });
 }

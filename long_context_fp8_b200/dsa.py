@@ -661,9 +661,13 @@ def dsa_blocks_extend(pool: dict, new_lens, page_size: int, num_pages: int, max_
     bt = pool["block_table"]
     if plan is None:
         i32 = dict(dtype=torch.int32, device=bt.device)
-        plan = {"token_start": torch.empty(bt.shape[0] + 1, **i32), "seq_ids": torch.empty(max_tokens, **i32),
-                "positions": torch.empty(max_tokens, **i32),
-                "slots": torch.empty(max_tokens, dtype=torch.int64, device=bt.device)}
+        with torch.cuda.stream(stream):        # None: as it is
+            plan = {"token_start": torch.empty(bt.shape[0] + 1, **i32), "seq_ids": torch.empty(max_tokens, **i32),
+                    "positions": torch.empty(max_tokens, **i32),
+                    "slots": torch.empty(max_tokens, dtype=torch.int64, device=bt.device)}
+        if stream is not None:
+            for t in plan.values():
+                t.record_stream(torch.cuda.current_stream(t.device))
     (_bound or _binding()).blocks_extend(bt, pool["context_lens"], pool["pages_held"], pool["free_pages"],
                                          pool["free_count"], new_lens, page_size, num_pages, max_tokens,
                                          plan["token_start"], plan["seq_ids"], plan["positions"], plan.get("slots"),

@@ -938,6 +938,44 @@ def test_calls_on_tensors_of_a_stream():
     assert torch.equal(out, dsa.dsa_rope(x, pos, table)[0])
 
 
+def test_memory_of_calls_on_another_stream():
+    """With a stream argument, what the call allocates is that stream's: memory that the current stream takes
+    right after the call is not the workspace or an output of the call, which has not begun yet."""
+    rng = np.random.default_rng(24)
+    inp, _ = _tree_case(rng, [9, 5, 1], [3000, 2100, 40], 32, 2, 128, 64, False)
+    dev = {k: v.cuda() for k, v in inp.items()}
+    P, tokens = torch.rand((3, 1000), device="cuda"), _dev([1, 2, 3])
+    tree = (P, None, tokens, _dev([-1, 0, 1]), _dev([0, 3]), torch.rand(3, device="cuda"), torch.rand(1, device="cuda"))
+    x, pos, table = torch.randn((500, 4, 64), device="cuda"), _dev(np.arange(500)), dsa.dsa_rope_freqs(64)
+
+    pools = [dict(block_table=torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), context_lens=_dev([0, 0]),
+                  pages_held=_dev([0, 0]), free_pages=_dev(np.arange(8)), free_count=_dev([8])) for _ in range(2)]
+    grow = _dev([20, 30])
+
+    def calls(stream, blocks):
+        return [*dsa.dsa_tree_attn(dev, 9, 3000, stream=stream), *dsa.dsa_verify_tree(*tree, max_path=3, stream=stream),
+                *dsa.dsa_rope(x, pos, table, k=x, stream=stream),
+                *dsa.dsa_blocks_extend(blocks, grow, 16, 8, 64, stream=stream).values()]
+
+    want = calls(None, pools[0])
+    torch.cuda.synchronize()
+    held = torch.cuda.Stream()
+    # freed blocks of every size in the current stream's pool, which a call must not take
+    pool = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (*[512] * 16, *[1 << 18] * 8, *[1 << 25] * 4)]
+    del pool
+    torch.cuda.synchronize()
+    with torch.cuda.stream(held):
+        torch.cuda._sleep(50_000_000)
+    got = calls(held, pools[1])
+    sizes = (*[512] * 64, *[4096] * 16, *[1 << 18] * 16, *[1 << 25] * 4)
+    taken = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    for t in taken:
+        assert bool((t == 0x7f).all())
+
+
 def test_binding_refusals():
     """What the binding checks before the library sees it: types, shapes, layouts and places of the tensors."""
     rng = np.random.default_rng(23)
