@@ -783,9 +783,10 @@ dsa_status dsa_profile_read(double *ms_out, int64_t *launches_out);
  * counterpart on the pages; off by default).  It arms a one-shot fault on the
  * host side: the next launch of the named tcgen05 indexer (the prefill one,
  * inside dsa_prefill / dsa_index_scores, or the decode one, inside
- * dsa_decode) has its producer warp in CTA 0 stop early (before its second
- * query copy in the prefill indexer, before its first copy in the decode
- * one), so the CTA's consumer waits for data that never comes.  That wait gives up
+ * dsa_decode) or of dsa_tree_attn has its producer warp in CTA 0 stop early
+ * (before its second query copy in the prefill indexer, before its first copy
+ * in the decode one, before its fifth tile of K or V in the tree attention), so
+ * the CTA's consumers wait for data that never comes.  That wait gives up
  * after its limit (2 s); the CTA records DSA_ERR_TIMEOUT in the workspace
  * status word, lets the copies and MMAs it did issue land, frees its tensor
  * memory and returns; the other CTAs finish normally, and the context stays
@@ -795,7 +796,8 @@ dsa_status dsa_profile_read(double *ms_out, int64_t *launches_out);
 typedef enum dsa_stall_target {
     DSA_STALL_NONE = 0,
     DSA_STALL_PREFILL_INDEXER = 1,
-    DSA_STALL_DECODE_INDEXER = 2
+    DSA_STALL_DECODE_INDEXER = 2,
+    DSA_STALL_TREE_ATTN = 3
 } dsa_stall_target;
 dsa_status dsa_test_stall_next(dsa_stall_target target);
 

@@ -445,8 +445,9 @@ extern "C" {
 dsa_status dsa_test_stall_next(dsa_stall_target target)
 {
     if (target == DSA_STALL_NONE) { g_test_stall.store(0); return DSA_OK; }
-    if (target != DSA_STALL_PREFILL_INDEXER && target != DSA_STALL_DECODE_INDEXER) return DSA_ERR_INVALID_ARG;
-    g_test_stall.store(target == DSA_STALL_PREFILL_INDEXER ? 1 : 2);
+    if (target != DSA_STALL_PREFILL_INDEXER && target != DSA_STALL_DECODE_INDEXER && target != DSA_STALL_TREE_ATTN)
+        return DSA_ERR_INVALID_ARG;
+    g_test_stall.store((int)target);
     return DSA_OK;
 }
 

@@ -10,7 +10,7 @@
 namespace dsa {
 
 // ---- test hook (api.cu): true once after dsa_test_stall_next armed `target`
-// (0: the prefill indexer, 1: the decode indexer); that launch leaves one copy
+// (0: the prefill indexer, 1: the decode indexer, 2: the tree attention); that launch leaves one copy
 // unissued so that a bounded wait runs out.
 bool consume_test_stall(int target);
 

@@ -36,7 +36,8 @@
 // With FP8 caches warp 0 brings codes, and eight more warps (12-15: K, 16-19: V) widen
 // them to bf16, exactly, into the ring; the scales stay in fp32 and multiply the logits
 // and the weights.
-// Every mbarrier wait is bounded (DSA_ERR_TIMEOUT on expiry).
+// Every wait of one role for another is on an mbarrier and bounded (DSA_ERR_TIMEOUT on expiry):
+// roles leave their loops one by one then, so a wait for all threads stands only behind the loops.
 //
 // Measured on one B200 (6.55 TB/s and 1.40 PFLOP/s sustained): 16 x 64K contexts, 8-16
 // drafts, 128 heads on one K/V head 0.56 ms back to back (1.1 PFLOP/s, 79 % of the sustained rate: the clock
@@ -89,6 +90,7 @@ struct TreeArgs {
     int tile_tok;                      // tokens of a tile (1 when group > 128)
     int head_tiles;                    // tiles of one token (1 when group <= 128)
     int cost_pair, cost_one;           // of a block of cache rows for a pair of tiles and for a single one
+    uint32_t stall_at;                 // test hook: CTA 0 stops before its K or V tile stall_at (~0: off)
     float scale_log2;
     uint16_t *out;
     float *lse;
@@ -118,7 +120,7 @@ template <bool KV8, int D> struct Smem {
     static constexpr int parent_off = mask_off + DSA_MAX_TREE * 16;
     static constexpr int seg_off = parent_off + DSA_MAX_TREE * 2;        // ring of segments
     static constexpr int bar_off = seg_off + TA_SEGS * 48;
-    static constexpr int n_bars = 2 + 2 * slots + 12 + 4 + 2 * TA_SEGS + 2 * codes;
+    static constexpr int n_bars = 2 + 2 * slots + 12 + 5 + 2 * TA_SEGS + 2 * codes;
     static constexpr int ctl_off = bar_off + 8 * n_bars;
     static constexpr int total = ctl_off + 256;
 };
@@ -311,7 +313,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::bar_off);
     uint64_t *qfull = bars, *qempty = bars + 1, *kvfull = bars + 2, *kvempty = kvfull + SLOTS;
     uint64_t *sfull = kvempty + SLOTS, *pfull = sfull + 4, *pvdone = pfull + 4, *oempty = pvdone + 4;   // [set][buffer]
-    uint64_t *mfull = oempty + 2, *mempty = mfull + 1, *gfull = mempty + 1, *gempty = gfull + TA_SEGS;
+    uint64_t *mfull = oempty + 2, *mempty = mfull + 1, *mlfull = mempty + 1, *gfull = mlfull + 1, *gempty = gfull + TA_SEGS;
     uint64_t *cfull = gempty + TA_SEGS, *cempty = cfull + CODES;
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + S::ctl_off);
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask_off);
@@ -340,6 +342,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
         mbar_init(&oempty[1], 8);
         mbar_init(mfull, 1);
         mbar_init(mempty, 8);
+        mbar_init(mlfull, 8);
         for (int i = 0; i < TA_SEGS; ++i) { mbar_init(&gfull[i], 1); mbar_init(&gempty[i], KV8 ? 19 : 11); }
         if (KV8)
             for (int i = 0; i < CODES; ++i) { mbar_init(&cfull[i], 1); mbar_init(&cempty[i], 4); }
@@ -445,6 +448,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             uint32_t t = 0;                        // tiles issued
             int item = 0;
             bool was_single = false, ok = true;
+            const uint32_t stall_at = blockIdx.x == 0 ? a.stall_at : ~0u;
             for (; ok && next(g); ++item) {
                 int row = cache_row(a, g.b, g.ctx, g.blk0 * TA_BLK + box * a.box, ctl);
                 if (lane == 0) {
@@ -479,6 +483,7 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                         const uint32_t ph = KV8 ? t / CODES : t / SLOTS;
                         ok = wait_or_abort(KV8 ? &cempty[st] : &kvempty[st], (ph & 1) ^ 1, &ctl->abort);
                         ok = __all_sync(0xffffffffu, ok);
+                        if (t == stall_at) ok = false;         // test hook: leave the copies unissued
                         if (!ok) break;
                         uint64_t *full = KV8 ? &cfull[st] : &kvfull[st];
                         if (lane == 0) {
@@ -892,10 +897,15 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             float m_o = -INFINITY, l_o = 0.f;      // the other set's part of the row
             if (!g.pair) {
                 // two copies in turn: a set may be an item ahead of the other, which still reads
-                float *ml = reinterpret_cast<float *>(smem + S::ml_off) + (singles++ & 1) * 512;
+                float *ml = reinterpret_cast<float *>(smem + S::ml_off) + (singles & 1) * 512;
                 ml[x * 256 + r] = m;
                 ml[x * 256 + 128 + r] = l;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                __syncwarp();
+                if (!dead) {                       // (a warp that gave up does not meet the others: their wait ends too)
+                    if (lane == 0) mbar_arrive(mlfull);
+                    if (!__all_sync(0xffffffffu, wait_or_abort(mlfull, singles & 1, &ctl->abort))) dead = true;
+                }
+                ++singles;
                 m_o = ml[(x ^ 1) * 256 + r];
                 l_o = ml[(x ^ 1) * 256 + 128 + r];
                 // (both sets have taken the same steps)
@@ -1240,6 +1250,7 @@ cudaError_t launch_tree_attn(const uint16_t *q, const void *k, const float *ks, 
     // measured a block: bf16 2.1 us for a pair and 1.3 for one, FP8 3.1 and 2.2 (the conversion is the same)
     a.cost_pair = ks ? 7 : 5;
     a.cost_one = ks ? 5 : 3;
+    a.stall_at = consume_test_stall(2 /* tree attention */) ? 4 : ~0u;
     a.scale_log2 = sm_scale * kLog2e;
     a.out = out;
     a.lse = lse;

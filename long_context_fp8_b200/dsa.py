@@ -748,10 +748,10 @@ def profile_read():
     return {name: (ms[i], n[i]) for i, name in enumerate(STAGES)}
 
 
-STALL_NONE, STALL_PREFILL_INDEXER, STALL_DECODE_INDEXER = 0, 1, 2
+STALL_NONE, STALL_PREFILL_INDEXER, STALL_DECODE_INDEXER, STALL_TREE_ATTN = 0, 1, 2, 3
 
 
 def test_stall_next(target: int):
     """Arm the library's one-shot test hook: the next launch of the named
-    indexer leaves one copy unissued, so that its bounded wait runs out."""
+    kernel leaves copies unissued, so that its bounded waits run out."""
     _check("dsa_test_stall_next", load().dsa_test_stall_next(int(target)))
