@@ -670,8 +670,9 @@ dsa_status dsa_rope(const void *q, int64_t q_stride, int H_q, const void *k, int
  * child (the row counts as padding), and for a page id out of range (its
  * positions count as rows of zeros).  Cache rows at and behind
  * context_lens[b] have no effect, whatever they hold; K and V of the
- * positions before it must be finite.  A query that is not gives NaN in its own
- * row and head alone.
+ * positions before it must be finite.  A query that is not gives NaN (out and
+ * lse) in its own row and head alone, and so does a row whose logits all come
+ * out as -infinity; in a padding row neither has an effect.
  * FP8 caches: K's scale is applied to the fp32 logits and V's to the fp32
  * weights, so that the codes enter the products exactly; weights are rounded
  * to bf16 once, as with bf16 caches.

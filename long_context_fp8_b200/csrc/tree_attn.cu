@@ -50,6 +50,7 @@
 // kernel from 450 to 358 us.  128-row steps over one score buffer: bf16 585, FP8 432 us.
 #include <algorithm>
 #include <atomic>
+#include <limits>
 #include <numeric>
 
 #include <cuda_fp8.h>
@@ -69,7 +70,10 @@ constexpr int TA_SEGS = 4;             // segments in the ring
 constexpr int TA_HALF = 64;            // cache rows of a step of a softmax set
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNaN = std::numeric_limits<float>::quiet_NaN();
 constexpr float kRescaleThreshold = 8.f;   // log2 units
+// A padding row's log2 sum in the workspace.  No other row has it: an infinite logit makes the sum a NaN.
+constexpr float kPadding = INFINITY;
 
 // Register splits: they add up to the launch's registers only for kernels built with
 // exactly these counts (checked by the build and before every launch).
@@ -97,7 +101,7 @@ struct TreeArgs {
     int4 *desc;                        // [CTAs] first item of each CTA: sequence, head, tile, bits (1: cut, 2: pair)
     uint32_t *err;                     // [CTAs] dsa_status
     float *part;                       // [2 CTAs][d / 4][256][4] O / l: slot, columns, row
-    float *part_lse;                   // [2 CTAs][256] log2 sum
+    float *part_lse;                   // [2 CTAs][256] log2 sum, kPadding for a padding row
     WsHeader *hdr;
 };
 
@@ -893,7 +897,10 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             need_masks();
             const uint32_t *mw = masks + 4 * node;
             const bool lives = valid && !dead && ((mw[node >> 5] >> (node & 31)) & 1u);
-            if (!lives || m == -INFINITY) l = 0.f;                   // a padding row: zeros and -inf
+            // A padding row: zeros and -inf.  A row that lives has at least its own logit, so a sum of 0 over all
+            // of it says that every logit is -inf, and its softmax is 0 / 0; a sum that is a NaN (of logits that
+            // are: the maximum may still be -inf, from masked columns) stays one.
+            if (!lives) l = 0.f;
             float m_o = -INFINITY, l_o = 0.f;      // the other set's part of the row
             if (!g.pair) {
                 // two copies in turn: a set may be an item ahead of the other, which still reads
@@ -919,12 +926,11 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
             }
             tc_fence_after();
             const float mt = fmaxf(l > 0.f ? m : -INFINITY, l_o > 0.f ? m_o : -INFINITY);
-            // (a sum that is no number, from a query that is none, stays one)
             const float f_own = l != 0.f ? exp2f(m - mt) : 0.f, f_oth = l_o != 0.f ? exp2f(m_o - mt) : 0.f;
             const float lt = l * f_own + l_o * f_oth;
-            const float inv = lt != 0.f ? 1.f / lt : 0.f;
-            const float g_own = f_own * inv, g_oth = f_oth * inv;
             const bool whole = g.blk0 == 0 && g.blk1 == s.nblk;
+            const float inv = lt != 0.f || (whole && lives) ? 1.f / lt : 0.f;
+            const float g_own = f_own * inv, g_oth = f_oth * inv;
             // slot 0: an item that began in an earlier CTA, 1: one that ends in a later CTA
             const int64_t pslot = (int64_t)blockIdx.x * 2 + (g.blk0 > 0 ? 0 : 1);
             const int prow = (g.pair ? x * 128 : 0) + r;
@@ -967,9 +973,8 @@ __device__ __forceinline__ void tree_attn_body(const CUtensorMap &qmap, const CU
                 }
             }
             if (valid && (g.pair || x == 0)) {
-                const float l2 = lives && lt != 0.f ? mt + log2f(lt) : -INFINITY;
-                if (!whole) a.part_lse[pslot * 256 + prow] = l2;
-                else if (a.lse) a.lse[orow] = lives && lt != 0.f ? mt * kLn2 + logf(lt) : -INFINITY;
+                if (!whole) a.part_lse[pslot * 256 + prow] = !lives ? kPadding : lt != 0.f ? mt + log2f(lt) : -INFINITY;
+                else if (a.lse) a.lse[orow] = !lives ? -INFINITY : lt != 0.f ? mt * kLn2 + logf(lt) : kNaN;
             }
             tc_fence_before();
             fence_proxy_async_smem();              // ml, before TMA may write Q there
@@ -1088,6 +1093,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
         const float4 *part = reinterpret_cast<const float4 *>(a.part) + quad * 256 + row;
         // one pass: sums relative to the largest part so far
         float M = -INFINITY, sum = 0.f;
+        bool padding = false;                  // (all parts say the same; the thread that writes has part 0)
         float4 acc[TM_QUADS];
 #pragma unroll
         for (int e = 0; e < TM_QUADS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1102,9 +1108,11 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
                 const int p = p0 + q * step;
                 if (p >= parts) continue;
                 L[q] = a.part_lse[at(p) * 256 + row];
+                padding |= L[q] == kPadding;
 #pragma unroll
                 for (int e = 0; e < TM_QUADS; ++e) o[q][e] = part[at(p) * (D / 4 * 256) + e * 256];
             }
+            if (padding) break;
 #pragma unroll
             for (int q = 0; q < TM_PARTS; ++q) {
                 top = fmaxf(top, L[q]);
@@ -1159,7 +1167,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
             if (begin == 1) continue;
         }
         if (!valid) continue;
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        const float inv = padding ? 0.f : 1.f / sum;           // 0 / 0 where no part has any weight
         const int64_t orow = (int64_t)(s.tok0 + tok) * a.H + d.y * a.group + head;
         uint4 *out = reinterpret_cast<uint4 *>(a.out + orow * D + quad * 4);
 #pragma unroll
@@ -1167,7 +1175,7 @@ tree_merge_kernel(const __grid_constant__ TreeArgs a, int ctas)
             out[e / 2] = make_uint4(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv),
                                     pack_bf16x2(acc[e + 1].x * inv, acc[e + 1].y * inv),
                                     pack_bf16x2(acc[e + 1].z * inv, acc[e + 1].w * inv));
-        if (quad == 0 && a.lse) a.lse[orow] = sum != 0.f ? M * kLn2 + logf(sum) : -INFINITY;
+        if (quad == 0 && a.lse) a.lse[orow] = padding ? -INFINITY : sum != 0.f ? M * kLn2 + logf(sum) : kNaN;
     }
 }
 
