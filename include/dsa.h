@@ -707,8 +707,12 @@ dsa_status dsa_tree_attn(const void *q, const void *k_cache, const float *k_cach
  * When no child is left the next token is drawn from R: the smallest v with
  * sum_{v' <= v} R(v') > u_sample[b] * sum R.  The emitted tokens then follow
  * the target's distribution exactly.
- * Sums and comparisons are in 64 bits, in a fixed order: a call repeats bit
- * for bit.  Outputs: path_out int32 [B, max_path]: the kept nodes, node 0
+ * Sums and comparisons are in 64 bits.  With point masses Z may follow from the
+ * last sum over the row, as long as at least an eighth of that sum is left.  The
+ * order of a sum depends on V, on B (a small batch has more SMs a sequence) and
+ * on where the row begins in memory (16 bytes), on nothing else: a call repeats bit for
+ * bit, and between batches of other sizes a sequence's sums may differ by their
+ * roundings.  Outputs: path_out int32 [B, max_path]: the kept nodes, node 0
  * first, then -1 (at most max_path nodes: the walk ends there);
  * accept_len int32 [B]: how many; next_token int32 [B].  A sequence without
  * tokens gets accept_len 0 and next_token -1; so does one that is reported as

@@ -248,6 +248,7 @@ verify_tree_kernel(const VerifyArgs a)
     bool summed = false;                       // warp_sum and block_sum belong to R
     bool known = false;                        // Z is the sum of R
     double Z = 1.0, total = 0.0;
+    double left = 1.0;                         // of the last sum over the row, since then
     move_to(0);
     if (writer && tid == 0) path[0] = 0;
     for (int i = 1; i < n && kept < a.max_path; ++i) {
@@ -276,9 +277,14 @@ verify_tree_kernel(const VerifyArgs a)
         __syncthreads();
         ++R.n;
         if (!R.q && known) {
-            // a point mass changes one entry: the sum follows without a pass, where enough is left of it
+            // A point mass changes one entry, and the sum follows from it without a pass.  That takes a part of
+            // the sum away and scales the rest back to one, the sum's error with it: each rejection multiplies the
+            // relative error by 1 / s.  So it is the product since the last pass that has to stay near one, and
+            // where less than an eighth is left the row is summed again: a rounding since then counts up to eight
+            // times in the sum.
             const double s = (Z - r_x) * f + fmax(r_x * f - 1.0, 0.0);
-            if (s > 0x1p-20 * (Z * f)) {
+            if (left * s >= 0.125) {
+                left *= s;
                 Z = s;
                 summed = false;
                 continue;
@@ -287,6 +293,7 @@ verify_tree_kernel(const VerifyArgs a)
         const double s = sum_row();
         if (s > 0.0) {
             Z = total = s;
+            left = 1.0;
             summed = known = true;
         } else {
             --R.n;                             // nothing would be left: R stays

@@ -6,7 +6,7 @@ import torch
 
 import spec_ref
 from long_context_fp8_b200 import dsa
-from test_gpu_spec import _run_tree, _tree_case
+from test_gpu_spec import _check_verify, _run_tree, _run_verify, _tree_case
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +53,51 @@ def test_tree_attn_queries_that_are_not_finite(ns, ctxs, H, kv8):
         assert torch.isnan(out[nan]).all() and torch.isnan(lse[nan]).all(), (value, where)
         assert torch.equal(out[~nan], base.cpu()[~nan]) and torch.equal(lse[~nan], base_lse.cpu()[~nan]), (value, where)
         assert torch.all(out[pad] == 0) and torch.isneginf(lse[pad]).all()
+
+
+# ------------------------------------------------------------------ peaked targets
+
+def _peaked(V, left, depth, ratio, u_last, rng):
+    """A root whose first `depth` children are point masses that each take all but `left` of what is left of the
+    target; one more child takes `ratio` of the rest."""
+    tokens = rng.permutation(V)[:depth + 1]
+    P = np.zeros((depth + 2, V))
+    rest = 1.0
+    for x in tokens[:depth]:
+        P[0, x] = rest * (1.0 - left)
+        rest *= left
+    others = np.setdiff1d(np.arange(V), tokens)
+    w = rng.random(len(others)) + 0.1
+    P[0, others] = rest * (1.0 - ratio) * w / w.sum()
+    P[0, tokens[depth]] = rest * ratio
+    P[1:] = 1.0 / V
+    n = depth + 2
+    u = np.full(n, 1.0 - 2.0 ** -24)                         # above 1 - left: rejected
+    u[depth + 1] = u_last
+    return P.astype(np.float32), np.append([0], tokens), np.array([-1] + [0] * (n - 1)), u.astype(np.float32)
+
+
+@pytest.mark.parametrize("B", [1, 9, 60, 500])
+@pytest.mark.parametrize("left", [6e-6, 2.0 ** -12, 0.1])
+def test_verify_peaked_targets_with_point_masses(left, B):
+    """Siblings that each leave little of the target: the sums after them keep their 64 bits, so the next child is
+    accepted or not as the definition has it, in batches of any size."""
+    V = 1003
+    rng = np.random.default_rng(5)
+    for depth in range(1, 8):
+        if left ** depth < 1e-30:
+            break
+        # the child's weight is `ratio` of the rest up to the roundings of P to fp32 (2^-24 each): u a few of them
+        # below and above it decides
+        for u_last in (0.5 - 2.0 ** -18, 0.5 + 2.0 ** -18):
+            P, tokens, parents, u = _peaked(V, left, depth, 0.5, u_last, rng)
+            n = len(tokens)
+            case = (np.tile(P, (B, 1)), None, np.tile(tokens, B), np.tile(parents, B), np.arange(B + 1) * n,
+                    np.tile(u, B), np.linspace(0.0, 0.999, B).astype(np.float32))
+            got = _run_verify(*case)
+            _check_verify(case, 128, got)
+            want = [0, depth + 1] if u_last < 0.5 else [0]
+            assert [int(v) for v in got[0][0] if v >= 0] == want
 
 
 # ------------------------------------------------------------------ bounded waits
