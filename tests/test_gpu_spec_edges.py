@@ -6,7 +6,7 @@ import torch
 
 import spec_ref
 from long_context_fp8_b200 import dsa
-from test_gpu_spec import _check_verify, _run_tree, _run_verify, _tree_case
+from test_gpu_spec import _check_verify, _dev, _run_tree, _run_verify, _tree_case
 
 pytestmark = pytest.mark.gpu
 
@@ -98,6 +98,50 @@ def test_verify_peaked_targets_with_point_masses(left, B):
             _check_verify(case, 128, got)
             want = [0, depth + 1] if u_last < 0.5 else [0]
             assert [int(v) for v in got[0][0] if v >= 0] == want
+
+
+# ------------------------------------------------------------------ idle sequences
+
+def _ms(call, times=5):
+    call()
+    best = float("inf")
+    for _ in range(times):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("B,max_tokens", [(1000, 64), (1000, 5000), (60000, 64), (200000, 5000)])
+def test_blocks_extend_over_idle_sequences(B, max_tokens):
+    """Runs of sequences that do not grow lie between the tokens of one group of four."""
+    new = np.zeros(B, int)
+    new[[0, 1, B // 2, B - 2, B - 1]] = [3, 2, 1, 4, 2]
+    pool = dict(block_table=np.full((B, 1), -1), context_lens=np.zeros(B, int), pages_held=np.zeros(B, int),
+                free_pages=np.arange(20), free_count=np.array([20]))
+    dev = {k: _dev(v) for k, v in pool.items()}
+    first = {k: v.clone() for k, v in dev.items()}
+    plan = dsa.dsa_blocks_extend(dev, _dev(new), 16, 20, max_tokens)
+    ref_plan, err = spec_ref.extend(pool, new, 16, 20, max_tokens)
+    assert not err
+    for got, ref in ((dev, pool), (plan, ref_plan)):
+        for k, v in ref.items():
+            assert np.array_equal(got[k].cpu().numpy(), v), k
+
+    def call(lens):
+        for k, v in first.items():
+            dev[k].copy_(v)
+        dsa.dsa_blocks_extend(dev, lens, 16, 20, max_tokens, plan=plan)
+
+    # the same tokens in one run of sequences: the gaps cost a search each, no walk
+    near = np.zeros(B, int)
+    near[:5] = new[new > 0]
+    near_dev, far_dev = _dev(near), _dev(new)
+    ms_near, ms_far = _ms(lambda: call(near_dev)), _ms(lambda: call(far_dev))
+    assert ms_far < 2.0 * ms_near + 0.02, (ms_near, ms_far)
 
 
 # ------------------------------------------------------------------ bounded waits
