@@ -264,7 +264,16 @@ struct Walker {
         while (true) {
             if (b >= a.B || item >= c1) return false;
             if (s.n == 0 || hk == a.Hkv) {
-                if (++b >= a.B) return false;
+                // The next sequence with tokens: 32 at a time (one at a time 60 000 idle ones took 4 ms).
+                for (++b;; b += 32) {
+                    if (b >= a.B) return false;
+                    const int c = b + (int)(threadIdx.x & 31);
+                    const unsigned any = __ballot_sync(0xffffffffu, c < a.B && a.token_start[c] != a.token_start[c + 1]);
+                    if (any) {
+                        b += __ffs(any) - 1;
+                        break;
+                    }
+                }
                 bool bad;
                 s.load(a, b, bad);
                 hk = rg = 0;

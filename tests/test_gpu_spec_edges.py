@@ -6,7 +6,7 @@ import torch
 
 import spec_ref
 from long_context_fp8_b200 import dsa
-from test_gpu_spec import _check_verify, _dev, _run_tree, _run_verify, _tree_case
+from test_gpu_spec import _check_tree, _check_verify, _dev, _run_tree, _run_verify, _tree_case
 
 pytestmark = pytest.mark.gpu
 
@@ -142,6 +142,28 @@ def test_blocks_extend_over_idle_sequences(B, max_tokens):
     near_dev, far_dev = _dev(near), _dev(new)
     ms_near, ms_far = _ms(lambda: call(near_dev)), _ms(lambda: call(far_dev))
     assert ms_far < 2.0 * ms_near + 0.02, (ms_near, ms_far)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_tree_attn_over_many_idle_sequences(kv8):
+    """Tens of thousands of sequences of which three have drafts, far apart."""
+    rng = np.random.default_rng(41)
+    inp, vals = _tree_case(rng, [3, 2, 4], [300, 700, 90], 16, 1, 128, 64, kv8)
+    B, at = 60000, [0, 29999, 59999]
+    n = np.zeros(B, int)
+    n[at] = [3, 2, 4]
+    ctx = np.full(B, -5)                                     # nothing is checked where there are no drafts
+    ctx[at] = [300, 700, 90]
+    bt = np.full((B, inp["block_table"].shape[1]), -1)
+    bt[at] = inp["block_table"].numpy()
+    dev = {k: v.cuda() for k, v in inp.items()}
+    dev.update(block_table=_dev(bt), context_lens=_dev(ctx), token_start=_dev(np.append([0], np.cumsum(n))))
+    ws = dsa.workspace(dsa.tree_attn_workspace_size(B, 9, 16, 1, 128), "cuda")
+    out, lse = dsa.dsa_tree_attn(dev, 4, 700, ws=ws)
+    assert dsa.dsa_stream_status(ws) == 0
+    _check_tree(inp, vals, out, lse, 128 ** -0.5)
+    ms = _ms(lambda: dsa.dsa_tree_attn(dev, 4, 700, out=out, lse=lse, ws=ws))
+    assert ms < 2.0, ms
 
 
 # ------------------------------------------------------------------ bounded waits
