@@ -677,7 +677,8 @@ dsa_status dsa_rope(const void *q, int64_t q_stride, int H_q, const void *k, int
  * weights, so that the codes enter the products exactly; weights are rounded
  * to bf16 once, as with bf16 caches.
  * Supported: d 64 or 128, page_size a multiple of 16, H_q a multiple of H_kv,
- * B <= 65536, num_pages * page_size < 2^31 (else DSA_ERR_UNSUPPORTED);
+ * B <= 65536, num_pages * page_size < 2^31, max_context or max_pages_per_seq *
+ * page_size at most 2^31 - 128 (else DSA_ERR_UNSUPPORTED);
  * sm_scale finite and > 0.  N == 0 is a no-op.  workspace: at least
  * dsa_tree_attn_workspace_size(...) bytes, 256-byte aligned; calls that may
  * overlap need one each.

@@ -155,6 +155,8 @@ dsa_status dsa_tree_attn(const void *q, const void *k_cache, const float *k_cach
     if (max_tree > DSA_MAX_TREE || (d != 64 && d != 128) || page_size % 16 != 0 || H_q % H_kv != 0 || H_q > 32768 ||
         B > 65536 || N > kInt32Max)
         return DSA_ERR_UNSUPPORTED;
+    // the kernel's positions are 32 bits wide, to the end of a context's last block of 128
+    if (std::min(max_context, (int64_t)max_pages_per_seq * page_size) > kInt32Max - 127) return DSA_ERR_UNSUPPORTED;
     if (!q || !k_cache || !v_cache || !block_table || !context_lens || !token_start || !parents || !out ||
         (k_cache_scale == nullptr) != (v_cache_scale == nullptr))
         return DSA_ERR_INVALID_ARG;

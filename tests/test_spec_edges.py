@@ -1,8 +1,15 @@
 """Host-only checks of the speculative-decoding operators at the edges of what their
 documentation allows."""
+import ctypes
 import os
 import re
 
+import pytest
+
+from long_context_fp8_b200 import build as dsa_build
+
+OK, INVALID, UNSUP, WS = 0, 1, 2, 3
+FAKE = ctypes.c_void_p(0x1000)           # never dereferenced: every call is refused
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "long_context_fp8_b200", "csrc")
 
 
@@ -22,3 +29,26 @@ def test_tree_attention_has_no_unbounded_wait_in_its_roles():
     roles = body[body.index("if (warp < 4 || warp >= 12)"):body.rindex("if (ctl->abort)")]
     assert roles.count("__syncthreads") == 1 and roles.rindex("__syncthreads") > roles.rindex("mbar_arrive(&oempty")
     assert "mbar_wait(" not in roles and "mbar_try_wait(" not in roles
+
+
+@pytest.fixture(scope="module")
+def lib():
+    dsa_build.build()
+    from long_context_fp8_b200 import dsa
+    return dsa.load()
+
+
+def test_tree_attention_refuses_contexts_whose_last_block_passes_32_bits(lib):
+    """Positions are counted in 32 bits up to the end of the last block of 128, which may lie past 2^31 where a
+    block table allows it (its pages may repeat)."""
+    def call(pages, ps, max_context, ws):
+        return lib.dsa_tree_attn(FAKE, FAKE, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, 20, pages, ps, 2, 10, 8, max_context,
+                                 16, 1, 128, 0.1, FAKE, None, FAKE, ws, None)
+
+    last = 2 ** 31 - 128
+    pages = (2 ** 31 - 16) // 16
+    for max_context in (2 ** 31 - 16, last + 1, 2 ** 40):
+        assert call(pages, 16, max_context, 0) == UNSUP, max_context
+    # one block less is refused for its workspace alone
+    assert call(pages, 16, last, 0) == WS
+    assert call(last // 16, 16, 2 ** 40, 0) == WS
