@@ -448,7 +448,9 @@ dsa_status dsa_quantize_e4m3(const void *x, dsa_dtype x_dtype, int64_t rows, int
  * [0, max_pages_per_seq * page_size) or whose page id is outside
  * [0, num_pages) is skipped, and DSA_ERR_INVALID_ARG is written to *status
  * (a device uint32_t the caller zeroes beforehand; nullable) unless it
- * already holds an error.  Supported: d_I a multiple of 8 up to 256, d a
+ * already holds an error.  Sequence -1 at position -1 is padding, as
+ * dsa_blocks_extend leaves it behind the last token: skipped without a report.
+ * Supported: d_I a multiple of 8 up to 256, d a
  * multiple of 8.  kidx_new, k_new, v_new, k_cache, v_cache 16-byte aligned,
  * kidx_cache 8-byte aligned.  N == 0 is a no-op.
  */

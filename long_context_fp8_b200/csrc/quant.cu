@@ -294,6 +294,7 @@ cache_append_kernel(const In *__restrict__ kidx_new, const uint16_t *__restrict_
     for (int64_t i = (int64_t)blockIdx.x * (QZ_THREADS / 32) + (threadIdx.x >> 5); i < N; i += warps) {
         const int b = __ldg(seq + i);
         const int64_t p = __ldg(pos + i);
+        if (b == -1 && p == -1) continue;            // padding, as dsa_blocks_extend leaves it behind the last token
         int64_t page = -1;
         if (b >= 0 && b < B && p >= 0 && p < (int64_t)max_pages * ps) page = __ldg(bt + (int64_t)b * max_pages + p / ps);
         if (page < 0 || page >= num_pages) {         // warp-uniform: every lane read the same token

@@ -6,7 +6,7 @@ import torch
 
 import spec_ref
 from long_context_fp8_b200 import dsa
-from test_gpu_spec import _check_tree, _check_verify, _dev, _run_tree, _run_verify, _tree_case
+from test_gpu_spec import INVALID, _check_tree, _check_verify, _dev, _run_tree, _run_verify, _status, _Step, _tree_case
 
 pytestmark = pytest.mark.gpu
 
@@ -164,6 +164,122 @@ def test_tree_attn_over_many_idle_sequences(kv8):
     _check_tree(inp, vals, out, lse, 128 ** -0.5)
     ms = _ms(lambda: dsa.dsa_tree_attn(dev, 4, 700, out=out, lse=lse, ws=ws))
     assert ms < 2.0, ms
+
+# ------------------------------------------------------------------ steps of fixed buffers over ragged drafts
+
+class _Ragged(_Step):
+    """A step whose buffers hold the most tokens that any step may have: sequences bring 0 to n drafts, and the rows
+    behind the last token are padding."""
+
+    def fill_ragged(self, seed):
+        self.fill(seed)
+        rng = np.random.default_rng(100 + seed)
+        self.ns = rng.integers(0, self.n + 1, self.B)
+        self.ns[seed % self.B], self.ns[(seed + 1) % self.B] = 0, self.n
+        parents, depth = np.full(self.N, 99), np.full(self.N, -7)
+        at = 0
+        for n in self.ns:
+            for i in range(n):
+                parents[at + i] = -1 if i == 0 else rng.integers(max(0, i - 3), i)
+                depth[at + i] = 0 if i == 0 else depth[at + parents[at + i]] + 1
+            at += n
+        self.start = np.append([0], np.cumsum(self.ns))
+        self.new.copy_(_dev(self.ns))
+        self.parents.copy_(_dev(parents))
+        self.depth.copy_(_dev(depth))
+        self.q[at:] = float("nan")
+        self.target[at:] = float("nan")
+
+    def run(self):
+        start, pool = self.plan["token_start"], self.pool
+        dsa.dsa_blocks_extend(pool, self.new, self.ps, self.P, self.N, plan=self.plan, status=self.status)
+        prefix = (pool["context_lens"] - (start[1:] - start[:-1]))[self.plan["seq_ids"].long().clamp(min=0)]
+        dsa.dsa_rope(self.q, prefix + self.depth, self.table, k=self.k, rot_begin=64, interleaved=True, q_out=self.qr,
+                     k_out=self.kr)
+        bt = pool["block_table"]
+        self.append(self.caches, self.kidx, self.kr.view(self.N, -1), self.v, self.plan["seq_ids"],
+                    self.plan["positions"], bt, status=self.status)
+        inp = dict(q=self.qr, block_table=bt, context_lens=pool["context_lens"], token_start=start, parents=self.parents,
+                   **{k: v for k, v in self.caches.items() if k[0] in "kv" and k[1] == "_"})
+        dsa.dsa_tree_attn(inp, self.n, self.max_context, out=self.out, lse=self.lse, ws=self.ws)
+        dsa.dsa_verify_tree(self.target, self.draft, self.tokens, self.parents, start, self.ua, self.us, path=self.path,
+                            accept_len=self.acc, next_token=self.next, status=self.status)
+        dsa.dsa_cache_compact(self.caches, bt, pool["context_lens"], start, self.path, self.acc, N=self.N,
+                              keep_lens=self.keep, status=self.status)
+        dsa.dsa_blocks_trim(pool, self.keep, self.ps, self.P, status=self.status)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_steps_of_fixed_buffers_over_ragged_drafts(kv8):
+    """One graph for every step, with as many rows as the largest: padding rows are no tokens to any operator, and
+    none of them is reported."""
+    B, ps, n, H, V = 5, 16, 7, 16, 300
+    s = _Ragged(B, ps, 12, 70, n, H, V, kv8)
+    rows = [[] for _ in range(B)]
+    graph = None
+    for seed in range(6):
+        s.fill_ragged(seed)
+        s.out.fill_(3.0)
+        s.lse.fill_(3.0)
+        if graph is None:
+            s.run()                                          # the library loads its kernels before the capture
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0 and dsa.dsa_stream_status(s.ws) == 0
+        total, start = int(s.start[-1]), s.start
+        assert torch.all(s.plan["seq_ids"][total:] == -1) and torch.all(s.plan["positions"][total:] == -1)
+        assert torch.all(s.out[total:] == 3.0) and torch.all(s.lse[total:] == 3.0)
+        _check_verify((s.target.cpu().numpy(), s.draft.cpu().numpy(), s.tokens.cpu().numpy(), s.parents.cpu().numpy(),
+                       start, s.ua.cpu().numpy(), s.us.cpu().numpy()), n, (s.path, s.acc, s.next))
+        acc, path = s.acc.cpu().numpy(), s.path.cpu().numpy()
+        for b in range(B):
+            t = slice(int(start[b]), int(start[b + 1]))
+            assert (acc[b] == 0) == (s.ns[b] == 0)
+            if s.ns[b]:
+                K, Vv = (torch.cat([torch.stack([r[j] for r in rows[b]]), new[t]]) if rows[b] else new[t]
+                         for j, new in enumerate((s.kr[:, 0], s.v)))
+                if kv8:
+                    K, Vv = ((c.view(torch.float8_e4m3fn).double() * sc.double()[:, None]) for c, sc in
+                             (dsa.dsa_quantize_e4m3(x.contiguous()) for x in (K, Vv)))
+                ro, rl, to, tl = spec_ref.tree_attn(s.qr[t].double().cpu().numpy(), K.double().cpu().numpy()[:, None],
+                                                    Vv.double().cpu().numpy()[:, None], len(K),
+                                                    s.parents[t].cpu().numpy(), H, 128 ** -0.5)
+                assert np.all(np.abs(s.out[t].double().cpu().numpy() - ro) <= to)
+                assert np.all(np.abs(s.lse[t].double().cpu().numpy() - rl) <= tl)
+            for i in range(acc[b]):
+                at = int(start[b]) + int(path[b, i])
+                rows[b].append((s.kr[at, 0].clone(), s.v[at].clone(), s.kidx[at].clone()))
+        ctx, held, bt = (s.pool[k].cpu().numpy() for k in ("context_lens", "pages_held", "block_table"))
+        count, free = int(s.pool["free_count"].item()), s.pool["free_pages"].cpu().numpy()
+        assert [len(r) for r in rows] == list(ctx) and np.array_equal(held, -(-ctx // ps))
+        pages = np.concatenate([free[:count]] + [bt[b, :held[b]] for b in range(B)])
+        assert np.array_equal(np.sort(pages), np.arange(70))
+        for b in range(B):
+            at = np.arange(ctx[b])
+            slot = torch.from_numpy(bt[b, at // ps].astype(np.int64) * ps + at % ps).cuda()
+            if len(at):
+                want = torch.stack([r[2] for r in rows[b]])
+                assert torch.equal(s.caches["kidx_cache"].flatten(0, 1)[slot], dsa.dsa_quantize_e4m3(want)[0])
+        if graph is None:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                s.run()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_append_reports_tokens_that_may_not_be_beside_padding(kv8):
+    """Only sequence -1 at position -1 is padding: one of the two alone is reported, as before."""
+    s = _Step(2, 16, 4, 8, 4, 4, 10, kv8)
+    s.pool["block_table"][:, 0] = torch.tensor([2, 5], dtype=torch.int32, device="cuda")
+    s.fill(1)
+    before = {k: v.clone() for k, v in s.caches.items()}
+    for seq, pos, want in (([-1] * 8, [-1] * 8, 0), ([-1] * 7 + [0], [-1] * 8, INVALID), ([-1] * 8, [-1] * 7 + [0], INVALID),
+                           ([-1] * 7 + [-2], [-1] * 8, INVALID)):
+        st = _status()
+        s.append(s.caches, s.kidx, s.k.view(8, -1), s.v, _dev(seq), _dev(pos), s.pool["block_table"], status=st)
+        assert int(st.item()) == want
+        assert all(torch.equal(s.caches[k], v) for k, v in before.items())
 
 
 # ------------------------------------------------------------------ bounded waits
