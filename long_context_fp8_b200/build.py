@@ -5,12 +5,14 @@ arch=compute_100a,code=sm_100a``) and links one shared library with the CUDA
 runtime linked statically, so the library depends on nothing but the driver.
 g++ compiles ``csrc/bind.cpp``, the Python binding of the speculative-decoding
 entry points, against the installed torch: ``long_context_fp8_b200/_bind.so``.
-Usable as ``python -m long_context_fp8_b200.build``.
+The library needs nvcc alone and is built first; without torch the binding is
+left out, with a note.  Usable as ``python -m long_context_fp8_b200.build``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import re
 import shutil
@@ -135,10 +137,17 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if force or not binding_up_to_date():
+    """Build the library, then the Python binding; returns the library's path."""
+    if force or not up_to_date():
+        build_library(verbose, extra_flags)
+    if importlib.util.find_spec("torch") is None:
+        print("no torch: the Python binding of the speculative-decoding entry points is not built", file=sys.stderr)
+    elif force or not binding_up_to_date():
         build_binding(verbose)
-    if not force and up_to_date():
-        return LIB
+    return LIB
+
+
+def build_library(verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     objs = []

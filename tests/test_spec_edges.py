@@ -3,6 +3,8 @@ documentation allows."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -52,3 +54,41 @@ def test_tree_attention_refuses_contexts_whose_last_block_passes_32_bits(lib):
     # one block less is refused for its workspace alone
     assert call(pages, 16, last, 0) == WS
     assert call(last // 16, 16, 2 ** 40, 0) == WS
+
+
+# ------------------------------------------------------------------ the build
+
+def test_library_is_built_first_and_without_torch(monkeypatch, capsys):
+    """The C library needs nvcc alone: it is built whether or not the Python binding can be."""
+    done = []
+    monkeypatch.setattr(dsa_build, "up_to_date", lambda: False)
+    monkeypatch.setattr(dsa_build, "binding_up_to_date", lambda: False)
+    monkeypatch.setattr(dsa_build, "build_library", lambda *a: done.append("library"))
+
+    def binding(*a):
+        done.append("binding")
+        raise RuntimeError("g++ failed")
+
+    monkeypatch.setattr(dsa_build, "build_binding", binding)
+    with pytest.raises(RuntimeError, match="g\\+\\+ failed"):        # loud, with the library in place
+        dsa_build.build()
+    assert done == ["library", "binding"]
+    done.clear()
+    monkeypatch.setattr(dsa_build.importlib.util, "find_spec", lambda name: None)
+    assert dsa_build.build() == dsa_build.LIB
+    assert done == ["library"] and "not built" in capsys.readouterr().err
+
+
+def test_build_runs_without_torch(tmp_path):
+    """The build script as a C user runs it, in an interpreter that has no torch."""
+    code = """
+import sys
+sys.path.insert(0, %r)
+from long_context_fp8_b200 import build
+build.BIND = %r                          # a binding that is not there yet
+print(build.build())
+""" % (dsa_build.ROOT, str(tmp_path / "_bind.so"))
+    # -S: no site-packages, and so no torch
+    r = subprocess.run([sys.executable, "-S", "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.strip() == dsa_build.LIB and not (tmp_path / "_bind.so").exists()
