@@ -27,6 +27,7 @@ LIB = os.path.join(PKG, "libdsa_b200.so")
 BIND = os.path.join(PKG, "_bind.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
+BIND_KEY = os.path.join(BUILD_DIR, "_bind.key")    # what BIND was compiled against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -101,32 +102,56 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def build_binding(verbose: bool = False) -> str:
-    """Compile the Python binding against the installed torch."""
+def binding_command() -> list:
+    """The compiler's call for the binding, against the installed torch and this interpreter."""
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    tmp, libs = BIND + ".tmp", os.path.join(root, "lib")
+    libs = os.path.join(root, "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE]
     for p in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
         cmd += ["-isystem", p]
-    cmd += [BIND_SRC, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl",
-            "-Wl,-rpath," + libs]
+    return cmd + [BIND_SRC, "-o", BIND + ".tmp", "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+                  "-ldl", "-Wl,-rpath," + libs]
+
+
+def binding_key() -> str:
+    """What the binding was compiled against, as text: another torch or interpreter is another binary interface,
+    which the file's name does not show and an import may not notice."""
+    import sysconfig
+
+    import torch
+    return "\n".join([torch.__version__, str(torch.version.git_version), str(sysconfig.get_config_var("SOABI")),
+                      *(w.replace(ROOT, ".") for w in binding_command())])      # wherever the tree lies
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile the Python binding against the installed torch."""
+    cmd = binding_command()
     if verbose:
         print(" ".join(cmd), flush=True)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    if os.path.exists(BIND_KEY):
+        os.remove(BIND_KEY)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND)
+    os.replace(BIND + ".tmp", BIND)
+    with open(BIND_KEY, "w") as f:
+        f.write(binding_key())
     return BIND
 
 
 def binding_up_to_date() -> bool:
-    return os.path.exists(BIND) and all(
-        os.path.getmtime(p) <= os.path.getmtime(BIND) for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not os.path.exists(BIND) or not os.path.exists(BIND_KEY):
+        return False
+    with open(BIND_KEY) as f:
+        if f.read() != binding_key():
+            return False
+    return all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:

@@ -92,3 +92,24 @@ print(build.build())
     r = subprocess.run([sys.executable, "-S", "-c", code], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == dsa_build.LIB and not (tmp_path / "_bind.so").exists()
+
+
+def test_binding_is_compiled_again_for_another_torch_or_interpreter(lib, monkeypatch):
+    """The binding's file says nothing about the torch and the interpreter it was compiled against."""
+    import sysconfig
+
+    import torch
+    assert dsa_build.binding_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.0.0")
+        assert not dsa_build.binding_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch.version, "git_version", "another commit")
+        assert not dsa_build.binding_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-39-x86_64-linux-gnu")
+        assert not dsa_build.binding_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(dsa_build, "nvcc", lambda: "/opt/another-cuda/bin/nvcc")
+        assert not dsa_build.binding_up_to_date()
+    assert dsa_build.binding_up_to_date()
