@@ -537,6 +537,12 @@ dsa_status dsa_decode_noalloc(const void *q_idx, const float *q_scale, const voi
  *   5. dsa_verify_tree walks the tree and samples the next token;
  *   6. dsa_cache_compact moves the accepted path's cache rows together;
  *   7. dsa_blocks_trim gives the other pages back.
+ * Several K/V heads: to steps 3 and 6 the heads of a position are one row, so
+ * bf16 caches [num_pages, page_size, H_kv, d] go there with H_kv * d for d.
+ * FP8 caches with H_kv > 1 are read by step 4 alone: the append and the
+ * compaction know one scale a row.  Step 3 writes index keys too; a cache that
+ * has none (a dense layer's, a drafter's) is filled by the caller, at step 1's
+ * slots, and compacted without them.
  * The drafted tokens of all sequences are packed: token_start int32 [B + 1],
  * ascending from 0, and sequence b's tokens are token_start[b] ..
  * token_start[b + 1] - 1.  `parents` int32, one per token: the parent's index

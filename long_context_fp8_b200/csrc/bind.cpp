@@ -386,9 +386,13 @@ PyObject *cache_compact(PyObject *, PyObject *const *a, Py_ssize_t n)
         arguments(n, 15);
         const Tensor &bt = reference(a[6]), &kc = as_tensor(a[2]), &path = as_tensor(a[9]);
         const Run run(a[14], bt);
-        if (bt.dim() != 2 || kc.dim() != 3 || path.dim() != 2)
-            throw Bad("expected block_table [B, max_pages], caches [P, page_size, d] and path [B, max_path]");
-        const int64_t B = bt.size(0), P = kc.size(0), ps = kc.size(1), d = kc.size(2), m = path.size(1);
+        if (bt.dim() != 2 || (kc.dim() != 3 && kc.dim() != 4) || path.dim() != 2)
+            throw Bad("expected block_table [B, max_pages], caches [P, page_size(, H_kv), d] and path [B, max_path]");
+        // the K/V heads of a position are one row to the library, which knows one scale a row
+        const int64_t heads = kc.dim() == 4 ? kc.size(2) : 1;
+        if (a[3] != Py_None && heads != 1) throw Bad("dsa_cache_compact takes FP8 caches of one K/V head");
+        const at::IntArrayRef scales = kc.sizes().slice(0, kc.dim() - 1);
+        const int64_t B = bt.size(0), P = kc.size(0), ps = kc.size(1), d = heads * kc.sizes().back(), m = path.size(1);
         int64_t d_I = 0;
         if (a[0] != Py_None) {
             const Tensor &ki = as_tensor(a[0]);
@@ -410,8 +414,8 @@ PyObject *cache_compact(PyObject *, PyObject *const *a, Py_ssize_t n)
                                  a[11] == Py_None ? INT32_MAX : as_int(a[11]), (int)m, (int)bt.size(1), P, (int)ps,
                                  (int)d_I, (int)d, optional(a[0], at::kByte, bt, {P, ps, d_I}),
                                  (float *)optional(a[1], at::kFloat, bt, {P, ps}), address(a[2], code, bt),
-                                 (float *)optional(a[3], at::kFloat, bt, {P, ps}), address(a[4], code, bt, kc.sizes()),
-                                 (float *)optional(a[5], at::kFloat, bt, {P, ps}), (int32_t *)lens.data_ptr(),
+                                 (float *)optional(a[3], at::kFloat, bt, scales), address(a[4], code, bt, kc.sizes()),
+                                 (float *)optional(a[5], at::kFloat, bt, scales), (int32_t *)lens.data_ptr(),
                                  status_word(a[13], bt), run.stream));
         return keep(a[12], lens);
     });

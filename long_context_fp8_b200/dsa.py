@@ -718,9 +718,9 @@ def dsa_verify_tree(target_probs, draft_probs, tokens, parents, token_start, u_a
 def dsa_cache_compact(caches: dict, block_table, context_lens, token_start, path, accept_len, N=None, keep_lens=None,
                       status=None, stream=None):
     """Move the accepted paths' rows together in the paged ``caches`` (updated
-    in place): k_cache, v_cache [P, page_size, d], bf16 or E4M3 codes with
-    k_cache_scale, v_cache_scale [P, page_size], and kidx_cache with
-    kscale_cache where given.  ``N`` bounds token_start (default: none).
+    in place): k_cache, v_cache bf16 [P, page_size(, H_kv), d], or E4M3 codes
+    of one K/V head with k_cache_scale, v_cache_scale [P, page_size], and
+    kidx_cache with kscale_cache where given.  ``N`` bounds token_start (default: none).
     Returns keep_lens int32 [B], the lengths to trim to."""
     get = caches.get
     return (_bound or _binding()).cache_compact(get("kidx_cache"), get("kscale_cache"), caches["k_cache"],

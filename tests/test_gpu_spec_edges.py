@@ -281,6 +281,92 @@ def test_append_reports_tokens_that_may_not_be_beside_padding(kv8):
         assert int(st.item()) == want
         assert all(torch.equal(s.caches[k], v) for k, v in before.items())
 
+# ------------------------------------------------------------------ several K/V heads
+
+def test_grouped_heads_through_append_attention_and_compaction():
+    """bf16 caches of several K/V heads: appended as rows of H_kv * d, attended, compacted in their own shape, and
+    attended again over what was accepted."""
+    rng = np.random.default_rng(61)
+    B, P, ps, H, Hkv, d = 3, 40, 16, 8, 4, 64
+    ns, first = np.array([5, 3, 7]), np.array([30, 0, 61])
+    N, start = int(ns.sum()), np.append([0], np.cumsum(ns))
+    K, V = (torch.from_numpy(rng.standard_normal((B, 80, Hkv, d))).bfloat16() for _ in range(2))
+    pool = dict(block_table=torch.full((B, 6), -1, dtype=torch.int32, device="cuda"), context_lens=_dev(np.zeros(B)),
+                pages_held=_dev(np.zeros(B)), free_pages=_dev(rng.permutation(P)), free_count=_dev([P]))
+    caches = dict(kidx_cache=torch.zeros((P, ps, 128), dtype=torch.uint8, device="cuda"),
+                  kscale_cache=torch.zeros((P, ps), device="cuda"),
+                  k_cache=torch.zeros((P, ps, Hkv, d), dtype=torch.bfloat16, device="cuda"),
+                  v_cache=torch.zeros((P, ps, Hkv, d), dtype=torch.bfloat16, device="cuda"))
+    rows = {**caches, "k_cache": caches["k_cache"].view(P, ps, Hkv * d), "v_cache": caches["v_cache"].view(P, ps, Hkv * d)}
+
+    def append(lens):
+        plan = dsa.dsa_blocks_extend(pool, _dev(lens), ps, P, int(np.sum(lens)))
+        seq, pos = plan["seq_ids"].cpu().long(), plan["positions"].cpu().long()
+        st = _status()
+        dsa.dsa_cache_append(rows, torch.randn((len(seq), 128)).bfloat16().cuda(), K[seq, pos].flatten(1).cuda(),
+                             V[seq, pos].flatten(1).cuda(), plan["seq_ids"], plan["positions"], pool["block_table"], status=st)
+        assert int(st.item()) == 0
+        return plan
+
+    def attend(lens, parents, q):
+        inp = dict(q=q.cuda(), k_cache=caches["k_cache"], v_cache=caches["v_cache"], block_table=pool["block_table"],
+                   context_lens=pool["context_lens"], token_start=_dev(np.append([0], np.cumsum(lens))), parents=_dev(parents))
+        return dsa.dsa_tree_attn(inp, 7, 96)
+
+    def check(out, lse, kv, ctxs, lens, parents, q):
+        at = 0
+        for b, n in enumerate(lens):
+            t = slice(at, at + n)
+            ro, rl, to, tl = spec_ref.tree_attn(q[t].double().numpy(), kv[0][b].double().numpy(), kv[1][b].double().numpy(),
+                                                int(ctxs[b]), parents[t], H // Hkv, d ** -0.5)
+            assert np.all(np.abs(out[t].double().cpu().numpy() - ro) <= to)
+            assert np.all(np.abs(lse[t].double().cpu().numpy() - rl) <= tl)
+            at += n
+
+    append(first)
+    plan = append(ns)
+    parents = np.concatenate([[-1] + [int(rng.integers(max(0, i - 2), i)) for i in range(1, n)] for n in ns])
+    q = torch.from_numpy(rng.standard_normal((N, H, d))).bfloat16()
+    check(*attend(ns, parents, q), [[x[b, :first[b] + n] for b, n in enumerate(ns)] for x in (K, V)], first + ns, ns,
+          parents, q)
+    path = np.array([[0, 2, 4], [0, 1, -1], [0, 3, 6]])
+    acc = np.array([3, 2, 3])
+    st = _status()
+    keep = dsa.dsa_cache_compact(caches, pool["block_table"], pool["context_lens"], plan["token_start"], _dev(path),
+                                 _dev(acc), N=N, status=st)
+    assert int(st.item()) == 0 and np.array_equal(keep.cpu().numpy(), first + acc)
+    dsa.dsa_blocks_trim(pool, keep, ps, P)
+    # what was accepted, in order; one more token each
+    kept = [[x[b, list(range(first[b])) + [first[b] + p for p in path[b, :acc[b]]]] for b in range(B)] for x in (K, V)]
+    for b in range(B):
+        for x, rest in zip((K, V), kept):
+            x[b, :len(rest[b])] = rest[b]
+    append(np.ones(B, int))
+    q = torch.from_numpy(rng.standard_normal((B, H, d))).bfloat16()
+    ctxs = first + acc + 1
+    check(*attend(np.ones(B, int), np.full(B, -1), q), [[x[b, :ctxs[b]] for b in range(B)] for x in (K, V)], ctxs, [1] * B,
+          np.full(B, -1), q)
+
+
+def test_compaction_takes_the_attention_caches_of_one_head():
+    """FP8 caches [P, page_size, 1, d] with their scales move like [P, page_size, d]; more heads are refused."""
+    rng = np.random.default_rng(62)
+    bt, ctx, start, path, acc = _dev([[3, 1]]), _dev([20]), _dev([0, 6]), _dev([[0, 2, 5]]), _dev([3])
+
+    def caches(*heads):
+        c = {x + "_cache": torch.from_numpy(rng.integers(0, 256, (5, 16, *heads, 64)).astype(np.uint8)).cuda() for x in "kv"}
+        c.update({x + "_cache_scale": torch.from_numpy(rng.random((5, 16, *heads)).astype(np.float32)).cuda() for x in "kv"})
+        return c
+
+    four = caches(1)
+    three = {k: v.squeeze(2).clone() for k, v in four.items()}
+    keep = [dsa.dsa_cache_compact(c, bt, ctx, start, path, acc) for c in (four, three)]
+    assert torch.equal(keep[0], keep[1]) and keep[0].tolist() == [17]
+    for k, v in three.items():
+        assert torch.equal(four[k].squeeze(2), v)
+    with pytest.raises(ValueError, match="one K/V head"):
+        dsa.dsa_cache_compact(caches(2), bt, ctx, start, path, acc)
+
 
 # ------------------------------------------------------------------ bounded waits
 
