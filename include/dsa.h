@@ -559,7 +559,8 @@ dsa_status dsa_decode_noalloc(const void *q_idx, const float *q_scale, const voi
  * pool, all device memory, updated in place:
  *   block_table  int32 [B, max_pages_per_seq]; context_lens int32 [B] (tokens
  *   cached); pages_held int32 [B] (pages in the table); free_pages int32
- *   [free_capacity], a stack of free page ids, its top at free_count - 1;
+ *   [free_capacity], a stack of free page ids, its top at free_count - 1
+ *   (NULL with free_capacity 0: every page is in the tables already);
  *   free_count int32 [1].
  * Sequence b grows by new_lens[b] >= 0 tokens.  With ps = page_size it needs
  *   need_b = max(0, ceil((context_lens[b] + new_lens[b]) / ps) - pages_held[b])

@@ -100,8 +100,8 @@ dsa_status dsa_blocks_extend(const int32_t *new_lens, int32_t *context_lens, int
     const dsa_status s = check_pages(max_pages_per_seq, num_pages, page_size);
     if (s != DSA_OK) return s;
     if (free_capacity > kInt32Max || max_tokens > kInt32Max) return DSA_ERR_UNSUPPORTED;
-    if (!new_lens || !context_lens || !pages_held || !block_table || !free_pages || !free_count || !token_start ||
-        (max_tokens > 0 && (!seq_ids || !positions)))
+    if (!new_lens || !context_lens || !pages_held || !block_table || (free_capacity > 0 && !free_pages) || !free_count ||
+        !token_start || (max_tokens > 0 && (!seq_ids || !positions)))
         return DSA_ERR_INVALID_ARG;
     if (!aligned(new_lens, 16) || !aligned(context_lens, 16) || !aligned(pages_held, 16) || !aligned(block_table, 16) ||
         !aligned(free_pages, 16) || !aligned(free_count, 4) || !aligned(token_start, 16) || !aligned(seq_ids, 16) ||
@@ -122,7 +122,7 @@ dsa_status dsa_blocks_trim(const int32_t *keep_lens, int32_t *context_lens, int3
     const dsa_status s = check_pages(max_pages_per_seq, num_pages, page_size);
     if (s != DSA_OK) return s;
     if (free_capacity > kInt32Max) return DSA_ERR_UNSUPPORTED;
-    if (!keep_lens || !context_lens || !pages_held || !block_table || !free_pages || !free_count)
+    if (!keep_lens || !context_lens || !pages_held || !block_table || (free_capacity > 0 && !free_pages) || !free_count)
         return DSA_ERR_INVALID_ARG;
     if (!aligned(keep_lens, 16) || !aligned(context_lens, 16) || !aligned(pages_held, 16) || !aligned(block_table, 16) ||
         !aligned(free_pages, 16) || !aligned(free_count, 4) || !aligned(status, 4))

@@ -6,7 +6,8 @@ import torch
 
 import spec_ref
 from long_context_fp8_b200 import dsa
-from test_gpu_spec import INVALID, _check_tree, _check_verify, _dev, _run_tree, _run_verify, _status, _Step, _tree_case
+from test_gpu_spec import (INVALID, WORKSPACE, _check_tree, _check_verify, _dev, _run_pool, _run_tree, _run_verify, _status,
+                           _Step, _tree_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -366,6 +367,24 @@ def test_compaction_takes_the_attention_caches_of_one_head():
         assert torch.equal(four[k].squeeze(2), v)
     with pytest.raises(ValueError, match="one K/V head"):
         dsa.dsa_cache_compact(caches(2), bt, ctx, start, path, acc)
+
+# ------------------------------------------------------------------ a pool without a stack
+
+def test_blocks_of_a_pool_whose_pages_are_all_in_the_tables():
+    """No free pages and no room for any: sequences grow and shrink within what they hold, the rest is refused."""
+    pool = dict(block_table=np.array([[3, 1, 4], [0, 5, -1], [2, -1, -1]]), context_lens=np.array([10, 0, 16]),
+                pages_held=np.array([3, 2, 1]), free_pages=np.zeros(0, int), free_count=np.array([0]))
+    dev, plan, st = _run_pool(pool, np.array([30, 32, 1]), 16, 6, 70)
+    ref_plan, err = spec_ref.extend(pool, np.array([30, 32, 1]), 16, 6, 70)
+    assert err and st == WORKSPACE
+    for got, ref in ((dev, pool), (plan, ref_plan)):
+        for k, v in ref.items():
+            assert np.array_equal(got[k].cpu().numpy(), v), k
+    keep, st = np.array([33, 30, 16]), _status()             # the third trim gives nothing back
+    dsa.dsa_blocks_trim(dev, _dev(keep), 16, 6, status=st)
+    assert not spec_ref.trim(pool, keep, 16, 6) and int(st.item()) == 0
+    for k, v in pool.items():
+        assert np.array_equal(dev[k].cpu().numpy(), v), k
 
 
 # ------------------------------------------------------------------ bounded waits
