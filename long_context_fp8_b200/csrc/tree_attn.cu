@@ -39,15 +39,16 @@
 // Every wait of one role for another is on an mbarrier and bounded (DSA_ERR_TIMEOUT on expiry):
 // roles leave their loops one by one then, so a wait for all threads stands only behind the loops.
 //
-// Measured on one B200 (6.55 TB/s and 1.40 PFLOP/s sustained): 16 x 64K contexts, 8-16
-// drafts, 128 heads on one K/V head 0.56 ms back to back (1.1 PFLOP/s, 79 % of the sustained rate: the clock
-// falls to 1.7 GHz under the power limit, and half of the exponentials on the FMA pipe took
-// 15 % fewer clocks but more power, and so more time); 64 x 32K, one draft, pages of
-// 128 rows 145 us (5.5 TB/s, 84 %; with pages of 16 rows, whose boxes are 2 KB, 4.2); FP8 64 x 32K x
-// 2-3 drafts 0.33 ms, bound by the widening and by shared memory, which the products,
-// the widening and the scales share.  The code of the hot roles has to fit the
-// instruction cache: one copy of each product's code instead of four took the FP8
-// kernel from 450 to 358 us.  128-row steps over one score buffer: bf16 585, FP8 432 us.
+// Measured on one B200 (6.55 TB/s and 1.40 PFLOP/s sustained), over a second of calls and "at first", in the
+// milliseconds before the power limit takes the SM clock down from 1.97 GHz to what is given here.
+// 16 x 64K contexts, 8-16 drafts, 128 heads on one K/V head: 0.65 ms at 1.5 GHz (0.89 PFLOP/s, 63 % of the
+// sustained rate), 0.55 ms at first (half of the exponentials on the FMA pipe took 15 % fewer clocks but more power,
+// and so more time).  64 x 32K, one draft, pages of 64 or 128 rows: 164 us (4.85 TB/s, 74 %), 147 at first; with
+// pages of 16 rows, whose boxes are 2 KB, 204 and 185.  FP8 64 x 32K x 2-3 drafts: 0.36 ms at 1.80 GHz, 0.33 at
+// first, bound by the widening and by shared memory, which the products, the widening and the scales share.  The
+// code of the hot roles has to fit the instruction cache: one copy of each product's code instead of four took the
+// FP8 kernel from 450 to 358 us (these and the next at first).  128-row steps over one score buffer: bf16 585, FP8
+// 432 us.
 #include <algorithm>
 #include <atomic>
 #include <limits>

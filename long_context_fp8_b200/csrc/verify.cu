@@ -5,7 +5,8 @@
 // rejection sums a whole row (Z = sum_v max(R(v) / Z - Q(v), 0)), and the last one is
 // drawn from.  So a sequence reads, besides single entries, one pair of rows for each
 // rejection, or the last node's target row alone if no child was left to reject; with point
-// masses one row for the first rejection and one for the draw, since the others change one entry.
+// masses one row for the first rejection and one for the draw, since the others change one entry (and one more
+// each time that less than an eighth of the last sum is left).
 //
 // A cluster of thread blocks takes a sequence.  Every block runs the same walk from
 // the same values; a row is cut into contiguous spans, one a warp, and each warp
