@@ -265,7 +265,7 @@ struct Walker {
         while (true) {
             if (b >= a.B || item >= c1) return false;
             if (s.n == 0 || hk == a.Hkv) {
-                // The next sequence with tokens: 32 at a time (one at a time 60 000 idle ones took 4 ms).
+                // The next sequence with tokens: 32 at a time (a call over 60 000 idle ones 4.0 ms one at a time, 0.3 so).
                 for (++b;; b += 32) {
                     if (b >= a.B) return false;
                     const int c = b + (int)(threadIdx.x & 31);
